@@ -21,15 +21,20 @@ QX_FLAG_PDL = 0x100
 QX_OK = 0
 QX_ERR_ARG, QX_ERR_FMT, QX_ERR_SHAPE, QX_ERR_ALIGN = -1, -2, -3, -4
 QX_ERR_MODE, QX_ERR_CUDA, QX_ERR_DEVICE_TIMEOUT, QX_ERR_UNSUPPORTED_DEVICE = -5, -6, -7, -8
+QX_ERR_RANGE = -9
 QX_MAX_MULTI = 8
 QX_MAX_COLS = 32768
 QX_CHAIN_MAX_JOBS = 128
 QX_CHAIN_MAX_ENTRIES = 4
+QX_F32, QX_F16, QX_BF16 = 0, 1, 30  # element types
+QX_MAX_HEAD_DIM = 256
+QX_MAX_GROUP = 128
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqx.so")
 
 EXPORTS = ["qx_quantize_act_q8", "qx_gemv", "qx_gemv_multi", "qx_gemm_prefill", "qx_gemm_prefill_ex",
            "qx_gemv_partials", "qx_gemv_chain", "qx_gemv_chain_noalloc", "qx_gemv_chain_scratch_bytes", "qx_row_bytes", "qx_repack",
+           "qx_rope_append", "qx_attn_paged", "qx_attn_shared", "qx_attn_scratch_bytes", "qx_block_norm",
            "qx_device_check", "qx_debug_timeout_probe", "qx_debug_mma_rate", "qx_debug_noalloc_fill",
            "qx_debug_trace_read", "qx_status_string", "qx_last_error", "qx_version"]
 
@@ -50,6 +55,29 @@ class _Job(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int), ("n", ctypes.c_int), ("W", ctypes.c_void_p * 4),
                 ("rows", ctypes.c_int64 * 4), ("y", ctypes.c_void_p * 4), ("cols", ctypes.c_int64),
                 ("x", ctypes.c_void_p)]
+
+
+class _Kv(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int), ("n_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("kv_len", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p), ("n_seqs", ctypes.c_int)]
+
+
+class _Qkv(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("n_q_heads", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int), ("res_dtype", ctypes.c_int),
+                ("y", ctypes.c_void_p), ("r", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("w_post", ctypes.c_void_p),
+                ("w_pre", ctypes.c_void_p), ("alpha", ctypes.c_float), ("eps", ctypes.c_float),
+                ("r_out", ctypes.c_void_p), ("x", ctypes.c_void_p), ("y_stride", ctypes.c_int64),
+                ("r_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("r_out_stride", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -78,6 +106,12 @@ def lib() -> ctypes.CDLL:
         L.qx_row_bytes.restype = ctypes.c_size_t
         L.qx_device_check.argtypes = [P]
         L.qx_repack.argtypes = [I, I, P, I64, I64, P, P]
+        L.qx_rope_append.argtypes = [P, P, P, P, I64, I, I, P, P]
+        L.qx_attn_paged.argtypes = [P, P, I64, I, I64, ctypes.c_float, I64, I64, P, I, P, P, P]
+        L.qx_attn_shared.argtypes = [P, P, I64, I, I64, ctypes.c_float, I64, P, I, P, P, P]
+        L.qx_attn_scratch_bytes.argtypes = [I64, I, I, I, I]
+        L.qx_attn_scratch_bytes.restype = ctypes.c_size_t
+        L.qx_block_norm.argtypes = [P, P]
         L.qx_debug_mma_rate.argtypes = [I, ctypes.POINTER(ctypes.c_double), P]
         L.qx_debug_timeout_probe.argtypes = [ctypes.c_uint64, P]
         L.qx_debug_noalloc_fill.argtypes = [ctypes.c_uint32, P]
@@ -91,7 +125,7 @@ def lib() -> ctypes.CDLL:
         for n in ("qx_quantize_act_q8", "qx_gemv", "qx_gemv_multi", "qx_gemm_prefill", "qx_gemm_prefill_ex",
                   "qx_gemv_partials", "qx_gemv_chain", "qx_gemv_chain_noalloc",
                   "qx_device_check", "qx_debug_timeout_probe",
-                  "qx_repack", "qx_debug_mma_rate", "qx_debug_noalloc_fill",
+                  "qx_repack", "qx_rope_append", "qx_attn_paged", "qx_attn_shared", "qx_block_norm", "qx_debug_mma_rate", "qx_debug_noalloc_fill",
                   "qx_debug_trace_read"):
             getattr(L, n).restype = I
         _lib = L
@@ -352,6 +386,230 @@ def qx_gemv_chain_noalloc(jobs, stream=None, marshalled=None):
     arr = marshalled if marshalled is not None else make_chain(jobs)
     _check(lib().qx_gemv_chain_noalloc(len(arr), arr, _stream(stream)), "qx_gemv_chain_noalloc")
     return jobs
+
+
+_DTYPE = {torch.float32: QX_F32, torch.float16: QX_F16, torch.bfloat16: QX_BF16}
+
+
+def _dtype(t: torch.Tensor, what: str) -> int:
+    try:
+        return _DTYPE[t.dtype]
+    except KeyError:
+        raise TypeError(f"{what}: {t.dtype} is not float32, float16 or bfloat16") from None
+
+
+def _heads(t: torch.Tensor, heads: int, dim: int, tokens: int, dtype, what: str) -> int:
+    """Token stride of a [tokens, heads, dim] CUDA tensor whose heads of a token lie one after another."""
+    if not t.is_cuda:
+        raise ValueError("qx operates on CUDA tensors only")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {t.dtype}, need {dtype}")
+    if t.shape != (tokens, heads, dim):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, need {(tokens, heads, dim)}")
+    a, b, c = t.stride()
+    if (c != 1 and dim > 1) or (b != dim and heads > 1):
+        raise ValueError(f"{what}: a token's heads must lie one after another (strides {(a, b, c)})")
+    return a if tokens > 1 else heads * dim
+
+
+class PagedKV:
+    """A paged key/value cache and the batch that calls run on (``qx_kv``).
+
+    k, v: float16 or bfloat16 [n_pages, heads, page_size, head_dim], the last
+    dimension contiguous (other orders as permuted views: a [page, slot, head,
+    dim] cache is ``cache.transpose(1, 2)``); table: int32 [n_seqs, pages];
+    kv_len: int32 [n_seqs]; q_start: int32 [n_seqs + 1].  The tensors are the
+    caller's: the program updates the contents of table, kv_len and q_start in
+    place from step to step (also between replays of a captured graph) and the
+    calls read them on the GPU.  The object keeps them alive, and the attention
+    calls' scratch, one for each stream."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor,
+                 q_start: torch.Tensor):
+        for t, what in ((k, "k"), (v, "v"), (table, "table"), (kv_len, "kv_len"), (q_start, "q_start")):
+            if not t.is_cuda:
+                raise ValueError("qx operates on CUDA tensors only")
+            if t.device != k.device:
+                raise ValueError(f"{what} is on {t.device}, k on {k.device}")
+        if k.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError("a cache holds float16 or bfloat16")
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v need one shape [n_pages, heads, page_size, head_dim], one type and one layout")
+        if k.stride(3) != 1:
+            raise ValueError("the elements of a head must be contiguous")
+        for t, what in ((table, "table"), (kv_len, "kv_len"), (q_start, "q_start")):
+            if t.dtype != torch.int32:
+                raise TypeError(f"{what}: {t.dtype}, need int32")
+            if not t.is_contiguous():
+                raise ValueError("qx needs contiguous tensors")
+        n = kv_len.numel()
+        if table.dim() != 2 or table.shape[0] != n or q_start.numel() != n + 1:
+            raise ValueError("table [n_seqs, pages], kv_len [n_seqs] and q_start [n_seqs + 1] differ in n_seqs")
+        self.k, self.v, self.table, self.kv_len, self.q_start = k, v, table, kv_len, q_start
+        self.dtype, self.device, self.n_seqs = k.dtype, k.device, n
+        pages, self.heads, self.page_size, self.head_dim = k.shape
+        self._c = _Kv(k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], self.heads, self.head_dim, self.page_size, pages,
+                      k.stride(0), k.stride(1), k.stride(2), table.data_ptr(), table.shape[1], kv_len.data_ptr(),
+                      q_start.data_ptr(), n)
+        self._ref = ctypes.byref(self._c)
+        self._scratch: dict = {}
+
+    def scratch(self, tokens: int, q_heads: int, stream: int) -> int:
+        """Address of the scratch of calls of at most these sizes on `stream` (grown when a call needs more)."""
+        have = self._scratch.get(stream)
+        if have is None or have[0] < tokens or have[1] < q_heads:
+            if have is not None:
+                tokens, q_heads = max(tokens, have[0]), max(q_heads, have[1])
+            need = int(lib().qx_attn_scratch_bytes(tokens, q_heads, self.heads, self.head_dim, self.n_seqs))
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device)):
+                buf = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.device)
+            have = self._scratch[stream] = (tokens, q_heads, buf, buf.data_ptr())
+        return have[3]
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def qx_rope_append(kv: PagedKV, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                   cos: torch.Tensor | None = None, sin: torch.Tensor | None = None, interleaved: bool = False,
+                   q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Rotate q [tokens, q_heads, dim] and k [tokens, heads, dim] by position, append k and v to the cache.
+
+    cos, sin: float32 [positions, rot / 2] (None: no rotation); interleaved:
+    pairs (2i, 2i + 1) instead of (i, i + rot / 2).  Returns the rotated
+    queries in the cache's type."""
+    n, dim, dt = k.shape[0], kv.head_dim, k.dtype
+    code = _dtype(k, "k")
+    a = _Qkv(n, 0, code, None, k.data_ptr(), v.data_ptr(), 0, _heads(k, kv.heads, dim, n, dt, "k"),
+             _heads(v, kv.heads, dim, n, dt, "v"))
+    out = None
+    if q is not None:
+        hq = q.shape[1]
+        a.n_q_heads, a.q, a.q_stride = hq, q.data_ptr(), _heads(q, hq, dim, n, dt, "q")
+        if q_out is None:
+            q_out = torch.empty((n, hq, dim), dtype=kv.dtype, device=kv.device)
+        elif q_out.dtype != kv.dtype or q_out.shape != q.shape or not q_out.is_contiguous() or not q_out.is_cuda:
+            raise ValueError("q_out: need a contiguous CUDA tensor of q's shape and the cache's type")
+        out = q_out.data_ptr()
+    cp = sp = None
+    n_pos = half = 0
+    if cos is not None:
+        if sin is None or cos.shape != sin.shape or cos.dim() != 2:
+            raise ValueError("cos and sin need one shape [positions, rot / 2]")
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32:
+            raise TypeError("cos and sin are float32")
+        n_pos, half = cos.shape
+        cp, sp = _ptr(cos), _ptr(sin)
+    _check(lib().qx_rope_append(kv._ref, ctypes.byref(a), cp, sp, n_pos, 2 * half, 1 if interleaved else 0, out,
+                                _raw_stream(stream, kv.device)), "qx_rope_append")
+    return q_out
+
+
+def _attn(kv: PagedKV, q: torch.Tensor, scale, out, lse, stream):
+    if q.dim() != 3:
+        raise ValueError("q: need [tokens, heads, dim]")
+    n, hq, dim = q.shape
+    q_stride = _heads(q, hq, kv.head_dim, n, kv.dtype, "q")
+    if out is None:
+        out = torch.empty((n, hq, dim), dtype=kv.dtype, device=kv.device)
+    elif out.shape != q.shape or not out.is_contiguous() or not out.is_cuda:
+        raise ValueError("out: need a contiguous CUDA tensor of q's shape")
+    lp = None
+    if lse is not None:
+        if lse.dtype != torch.float32:
+            raise TypeError("lse is float32")
+        lp = _ptr(_need(lse, n * hq * 4, "lse"))
+    s = _raw_stream(stream, kv.device)
+    return (kv._ref, q.data_ptr(), n, hq, q_stride, dim ** -0.5 if scale is None else scale), out, \
+        (out.data_ptr(), _dtype(out, "out"), lp, kv.scratch(n, hq, s), s)
+
+
+def qx_attn_paged(kv: PagedKV, q: torch.Tensor, scale: float | None = None, window: int = 0, sinks: int = 0,
+                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of q [tokens, q_heads, dim] over the cache; scale None: dim ** -0.5.
+
+    window > 0: a token sees the last `window` keys up to its own and the first
+    `sinks`.  out: the cache's type or float32; lse: float32 [tokens, q_heads],
+    filled with the rows' log-sum-exp."""
+    head, out, tail = _attn(kv, q, scale, out, lse, stream)
+    _check(lib().qx_attn_paged(*head, window, sinks, *tail), "qx_attn_paged")
+    return out
+
+
+def qx_attn_shared(kv: PagedKV, q: torch.Tensor, shared_len: int, scale: float | None = None,
+                   out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """qx_attn_paged for sequences that all begin with the same `shared_len` keys and values, read once for all."""
+    head, out, tail = _attn(kv, q, scale, out, lse, stream)
+    _check(lib().qx_attn_shared(*head, shared_len, *tail), "qx_attn_shared")
+    return out
+
+
+def _rows(t: torch.Tensor, shape, what: str) -> int:
+    """Row stride of a [rows, cols] CUDA tensor with contiguous rows."""
+    if not t.is_cuda:
+        raise ValueError("qx operates on CUDA tensors only")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, need {tuple(shape)}")
+    if t.stride(1) != 1 and shape[1] > 1:
+        raise ValueError(f"{what}: rows must be contiguous")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def qx_block_norm(y: torch.Tensor | None, r: torch.Tensor, w_post: torch.Tensor | None = None,
+                  gate: torch.Tensor | None = None, alpha: float = 1.0, w_pre: torch.Tensor | None = None,
+                  eps: float = 1e-5, r_out: torch.Tensor | None = None, x_out: torch.Tensor | None = None, stream=None):
+    """r' = r + alpha * gate * norm(y) and x = norm(r'), a row at a time; returns (r', x).
+
+    y (a block's output; None: x is the norm of r), gate ([rows, cols], or
+    [cols] for all rows) and x share a type, r and r' another; w_post (None:
+    y as it is) and w_pre (None: no x) are float32 [cols].  r_out may be r, and
+    x_out may be y."""
+    if r.dim() != 2:
+        raise ValueError("r: need [rows, cols]")
+    shape = r.shape
+    a = _Norm()
+    a.rows, a.cols = shape
+    act = y if y is not None else x_out
+    act_type = act.dtype if act is not None else r.dtype
+    a.dtype, a.res_dtype, a.alpha, a.eps = _DTYPE.get(act_type, -1), _DTYPE.get(r.dtype, -1), alpha, eps
+    if a.dtype < 0 or a.res_dtype < 0:
+        raise TypeError("qx_block_norm takes float32, float16 and bfloat16")
+    a.r, a.r_stride = r.data_ptr(), _rows(r, shape, "r")
+    if y is not None:
+        a.y, a.y_stride = y.data_ptr(), _rows(y, shape, "y")
+    if gate is not None:
+        if gate.dtype != act_type:
+            raise TypeError("gate has y's type")
+        if gate.dim() == 1:
+            a.gate, a.gate_stride = _ptr(_need(gate, shape[1] * gate.element_size(), "gate")), 0
+        else:
+            a.gate, a.gate_stride = gate.data_ptr(), _rows(gate, shape, "gate")
+    for w, what in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if w is not None:
+            if w.dtype != torch.float32:
+                raise TypeError(f"{what} is float32")
+            setattr(a, what, _ptr(_need(w, shape[1] * 4, what)))
+    if y is None and r_out is None:
+        r_out = r
+    else:
+        if r_out is None:
+            r_out = torch.empty_like(r, memory_format=torch.contiguous_format)
+        elif r_out.dtype != r.dtype:
+            raise TypeError("r_out has r's type")
+        a.r_out, a.r_out_stride = r_out.data_ptr(), _rows(r_out, shape, "r_out")
+    if w_pre is not None:
+        if x_out is None:
+            x_out = torch.empty(shape, dtype=act_type, device=r.device)
+        elif x_out.dtype != act_type:
+            raise TypeError("x_out has y's type")
+        a.x, a.x_stride = x_out.data_ptr(), _rows(x_out, shape, "x_out")
+    else:
+        x_out = None
+    _check(lib().qx_block_norm(ctypes.byref(a), _raw_stream(stream, r.device)), "qx_block_norm")
+    return r_out, x_out
 
 
 def qx_debug_mma_rate(kind: int, stream=None) -> float:

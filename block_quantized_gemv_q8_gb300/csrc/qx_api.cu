@@ -13,6 +13,7 @@
 
 #include "../../include/qx.h"
 #include "../../include/qx_debug.h"
+#include "qx_device.cuh"
 #include "qx_internal.h"
 
 namespace qx {
@@ -742,6 +743,19 @@ qx_status marshal_chain(int n_jobs, const qx_gemv_job* jobs, ChainParams& p) {
 
 }  // namespace
 
+// For the entry points in qx_layer_api.cu.
+namespace qx {
+qx_status current_device(int* sm_count, unsigned** err_word) {
+    DeviceInfo* dev = nullptr;
+    const qx_status st = device_info(&dev);
+    if (st != QX_OK) return st;
+    *sm_count = dev->sm_count;
+    *err_word = dev->err_word;
+    return QX_OK;
+}
+qx_status report_cuda(cudaError_t e, const char* where) { return e == cudaSuccess ? QX_OK : cuda_fail(e, where); }
+}  // namespace qx
+
 extern "C" {
 
 size_t qx_row_bytes(qx_fmt fmt, int64_t cols) {
@@ -894,7 +908,7 @@ qx_status qx_device_check(qx_stream_t s) {
         const unsigned zero = 0;
         if ((e = cudaMemcpyToSymbol(g_err_word, &zero, sizeof(zero))) != cudaSuccess)
             return cuda_fail(e, "cudaMemcpyToSymbol");
-        return QX_ERR_DEVICE_TIMEOUT;
+        return (word & ~kErrRange) ? QX_ERR_DEVICE_TIMEOUT : QX_ERR_RANGE;
     }
     return QX_OK;
 }
@@ -920,6 +934,7 @@ const char* qx_status_string(qx_status st) {
         case QX_ERR_DEVICE_TIMEOUT: return "QX_ERR_DEVICE_TIMEOUT: a kernel's bounded wait ran out";
         case QX_ERR_UNSUPPORTED_DEVICE:
             return "QX_ERR_UNSUPPORTED_DEVICE: the current device is not compute capability 10.3 (GB300)";
+        case QX_ERR_RANGE: return "QX_ERR_RANGE: a kernel met a page, length or position out of range";
         default: return "unknown qx status";
     }
 }
@@ -928,7 +943,8 @@ const char* qx_last_error(void) { return g_last_error; }
 
 const char* qx_version(void) {
     return "qx 0.2 sm_103a: actq8; gemv {q4_k,q6_k,q6_k_soa,q8_0} x {f32,w4a8,w4a8 fused} (bulk-copy stream, "
-           "pdl); multi; chain; partials; prefill {gemv per row, mma.sync, tcgen05, small batch}; repack";
+           "pdl); multi; chain; partials; prefill {gemv per row, mma.sync, tcgen05, small batch}; repack; "
+           "rope_append; attn {paged, shared}; block_norm";
 }
 
 // ----------------------------------------------------------------------------

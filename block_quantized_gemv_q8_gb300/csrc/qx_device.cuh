@@ -15,6 +15,7 @@ constexpr unsigned kErrTimeoutDrain = 4u;  // copies still in flight at exit
 constexpr unsigned kErrTimeoutProbe = 8u;  // the test probe's wait ran out
 constexpr unsigned kErrTimeoutMma = 16u;   // tensor-core pipeline wait ran out
 constexpr unsigned kErrTimeoutChain = 32u; // a chain job waited too long for the previous job
+constexpr unsigned kErrRange = 64u;        // a page, length or position out of range (not a wait)
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

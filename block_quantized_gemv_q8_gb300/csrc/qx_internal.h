@@ -192,4 +192,67 @@ bool prefill_tc_serves(int fmt, int64_t N, int64_t K, int64_t M, int64_t row_byt
 cudaError_t launch_prefill_tc(int fmt, const uint8_t* W, int64_t N, int64_t K, int64_t row_bytes, const int8_t* xq,
                               const float* xd, int64_t M, float* Y, unsigned* err, int sm_count, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Between the weight products (qx_rope.cu, qx_attn.cu, qx_norm.cu; entry points
+// in qx_layer_api.cu)
+// ---------------------------------------------------------------------------
+
+// The current device's SM count and error word (QX_ERR_UNSUPPORTED_DEVICE on
+// another GPU), and a CUDA failure as a status with its text kept.
+qx_status current_device(int* sm_count, unsigned** err_word);
+qx_status report_cuda(cudaError_t e, const char* where);
+
+// A paged cache as the kernels see it (qx_kv, checked).
+struct KvView {
+    char* k;
+    char* v;
+    int64_t page_stride, head_stride, slot_stride;  // elements
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* kv_len;
+    const int32_t* q_start;
+    int n_seqs, n_heads, head_dim;
+    int page_shift;   // page_size = 1 << page_shift
+    int n_pages;
+    unsigned* err;    // device error word
+};
+
+struct RopeParams {
+    KvView kv;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *cos, *sin;
+    int64_t n_pos;
+    void* q_out;
+    int n_tokens, n_q_heads, rot, interleaved;
+};
+
+struct AttnParams {
+    KvView kv;
+    const void* q;
+    int64_t q_stride;
+    void* out;
+    float* lse;
+    int n_tokens, n_q_heads, out_f32;
+    float scale_log2;  // scale * log2(e)
+    int64_t window;    // 0: none
+    int64_t sinks;
+    int64_t shared_len;
+    void* scratch;
+};
+
+struct NormParams {
+    const void *y, *r, *gate;
+    const float *w_post, *w_pre;
+    void *r_out, *x;
+    int64_t y_stride, r_stride, gate_stride, r_out_stride, x_stride;
+    int64_t rows;
+    int cols;
+    float alpha, eps;
+};
+
+cudaError_t launch_rope(int src, int dst, const RopeParams& p, int sm_count, cudaStream_t s);
+cudaError_t launch_attn(int dtype, const AttnParams& p, int sm_count, cudaStream_t s);
+cudaError_t launch_norm(int dtype, int res_dtype, const NormParams& p, bool vec, cudaStream_t s);
+
 }  // namespace qx

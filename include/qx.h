@@ -90,6 +90,7 @@ typedef int qx_status;
 #define QX_ERR_CUDA (-6)               /* a CUDA runtime call or launch failed    */
 #define QX_ERR_DEVICE_TIMEOUT (-7)     /* a kernel's bounded wait ran out         */
 #define QX_ERR_UNSUPPORTED_DEVICE (-8) /* current device is not compute 10.3      */
+#define QX_ERR_RANGE (-9)              /* a kernel met a page, length or position out of range */
 
 /* Largest activation width served (columns per row). */
 #define QX_MAX_COLS 32768
@@ -334,9 +335,162 @@ size_t qx_row_bytes(qx_fmt fmt, int64_t cols);
 qx_status qx_repack(qx_fmt from, qx_fmt to, const void* src, int64_t rows, int64_t cols, void* dst,
                     qx_stream_t s);
 
+/*
+ * Between the weight products of a decoder layer: keys and values appended to
+ * a paged cache with the position rotation applied on the way, attention over
+ * that cache, and the norms around a block.
+ *
+ * Element types (the GGML type ids).
+ */
+typedef enum { QX_F32 = 0, QX_F16 = 1, QX_BF16 = 30 } qx_dtype;
+
+/*
+ * A paged key/value cache and the batch that a call runs on (host struct; its
+ * pointers are device memory).  Key j of sequence b lies in page
+ * table[b * table_stride + j / page_size], slot j % page_size: element d of
+ * head h is k[page * page_stride + h * head_stride + slot * slot_stride + d]
+ * (strides in elements, the same for v), so both a [page, head, slot, d] and a
+ * [page, slot, head, d] cache can be described.  Sequence b brings the tokens
+ * q_start[b] .. q_start[b + 1] - 1 of the call, and kv_len[b] keys with those
+ * counted: token t of it stands at position
+ *     pos = kv_len[b] - (q_start[b + 1] - q_start[b]) + (t - q_start[b]).
+ * A token at a negative position is padding.  q_start is ascending from 0;
+ * tokens from q_start[n_seqs] on belong to no sequence and are left alone.
+ * table, kv_len and q_start are read when the kernels run, so a captured graph
+ * can be replayed with their contents changed.  A page number outside
+ * [0, n_pages), a key beyond table_stride * page_size or a position beyond
+ * the rotation's table is neither read nor written; qx_device_check() then
+ * returns QX_ERR_RANGE.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    qx_dtype dtype;       /* QX_F16 or QX_BF16                                  */
+    int n_heads;          /* key/value heads                                    */
+    int head_dim;         /* a multiple of 8, at most QX_MAX_HEAD_DIM           */
+    int page_size;        /* a power of two, 16 .. 65536                        */
+    int64_t n_pages;
+    int64_t page_stride;  /* elements, multiples of 8; k and v 16-byte aligned  */
+    int64_t head_stride;
+    int64_t slot_stride;
+    const int32_t* table;
+    int64_t table_stride; /* entries between the rows of table                  */
+    const int32_t* kv_len;
+    const int32_t* q_start;
+    int n_seqs;
+} qx_kv;
+#define QX_MAX_HEAD_DIM 256
+/* Most query heads that share a key head in the attention calls. */
+#define QX_MAX_GROUP 128
+
+/* The rows of a Q/K/V product (host struct, device pointers): token t's heads
+ * of head_dim elements lie one after another from t * stride elements on, so
+ * q, k and v may be parts of one buffer.  q may be NULL (n_q_heads 0). */
+typedef struct {
+    int64_t n_tokens;
+    int n_q_heads;
+    qx_dtype dtype;  /* QX_F32, QX_F16 or QX_BF16 */
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_stride; /* elements, multiples of 8; pointers 16-byte aligned */
+    int64_t k_stride;
+    int64_t v_stride;
+} qx_qkv;
+
+/*
+ * Rotate the queries and keys of the call's tokens by their position, write
+ * the keys and values to the cache and the queries to q_out (cache type,
+ * [n_tokens, n_q_heads, head_dim]).  With c = cos[pos, i], s = sin[pos, i]
+ * (device, f32 [n_pos, rot / 2]), i < rot / 2, and (a, b) the elements
+ * (i, i + rot / 2) of a head, or (2 i, 2 i + 1) where `interleaved` is set
+ * (GGUF's two conventions):  a' = a c - b s,  b' = b c + a s.  Elements from
+ * rot on pass.  The arithmetic is in f32, rounded once to the cache's type.
+ * rot is a multiple of 8, at most head_dim; 0 (cos and sin may be NULL)
+ * rotates nothing.  Padding tokens append nothing and get zeros in q_out.
+ * Two tokens of a call that share a slot race; a page may belong to several
+ * sequences as long as none of the call's tokens falls into it.
+ */
+qx_status qx_rope_append(const qx_kv* kv, const qx_qkv* in, const float* cos, const float* sin, int64_t n_pos,
+                         int rot, int interleaved, void* q_out, qx_stream_t s);
+
+/*
+ * Attention of the call's tokens over the cache (which holds their own keys
+ * already).  Query head h reads key head h / (n_q_heads / n_heads); row (t, h)
+ *     out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q . k_j),
+ * over the keys j <= pos that the window leaves: all of them for window 0,
+ * else j > pos - window or j < sinks (the first `sinks` keys stay visible).
+ * q: device, cache type, token stride q_stride elements (a multiple of 8; heads
+ * one after another); out: [n_tokens, n_q_heads, head_dim], the cache's type
+ * or QX_F32; lse (may be NULL): f32 [n_tokens, n_q_heads], the natural log of
+ * sum_j p_j.  A row that sees no key (a padding token) gets zeros and -inf.
+ * Scores, maxima, sums and outputs are held in f32; the probabilities are
+ * rounded to the cache's type before they meet v (relative 2^-8 for bf16,
+ * 2^-11 for f16, at most), so an f32 out carries that much too.
+ * Slots of the cache that no token of its sequence sees have no effect,
+ * whatever they hold (pages outside the window may be given back).
+ * scratch: device, qx_attn_scratch_bytes() of the same sizes, 256-byte
+ * aligned, zero-filled before its first use; a completed call leaves it fit
+ * for the next.  Calls that may overlap need separate scratch.
+ */
+qx_status qx_attn_paged(const qx_kv* kv, const void* q, int64_t n_tokens, int n_q_heads, int64_t q_stride,
+                        float scale, int64_t window, int64_t sinks, void* out, qx_dtype out_dtype, float* lse,
+                        void* scratch, qx_stream_t s);
+
+/*
+ * qx_attn_paged without a window for sequences whose first shared_len keys and
+ * values are the same: those keys are read through the first sequence's row of
+ * the table, once for the whole batch, and each sequence's own keys after
+ * them.  The caller guarantees that every sequence's keys below shared_len
+ * hold what the first one's do (usually they are the same pages).
+ * 0 <= shared_len <= kv_len[b] for every sequence.
+ */
+qx_status qx_attn_shared(const qx_kv* kv, const void* q, int64_t n_tokens, int n_q_heads, int64_t q_stride,
+                         float scale, int64_t shared_len, void* out, qx_dtype out_dtype, float* lse, void* scratch,
+                         qx_stream_t s);
+
+/* Device scratch bytes that qx_attn_paged and qx_attn_shared need on the
+ * current device for at most these sizes; 0 for invalid ones. */
+size_t qx_attn_scratch_bytes(int64_t n_tokens, int n_q_heads, int n_heads, int head_dim, int n_seqs);
+
+/*
+ * The step from one block of a layer to the next, a row at a time:
+ *     u  = y * w_post / sqrt(mean(y^2) + eps)     (w_post NULL: u = y)
+ *     r' = r + alpha * gate * u                   (gate NULL: 1)
+ *     x  = r' * w_pre / sqrt(mean(r'^2) + eps)    (w_pre NULL: no x)
+ * y, gate and x: dtype; r and r_out: res_dtype (each QX_F32, QX_F16 or
+ * QX_BF16); w_post and w_pre: f32 [cols].  Rows lie y_stride, gate_stride, ...
+ * elements apart (gate_stride 0: one gate for all rows).  y NULL: u = 0, so x
+ * is the norm of r.  r_out NULL: r' is not written.  The arithmetic is in f32;
+ * x comes from r' before it is rounded.  r_out may be r and x may be y.
+ * 1 <= cols <= QX_MAX_COLS.
+ */
+typedef struct {
+    int64_t rows;
+    int64_t cols;
+    qx_dtype dtype;
+    qx_dtype res_dtype;
+    const void* y;
+    const void* r;
+    const void* gate;
+    const float* w_post;
+    const float* w_pre;
+    float alpha;
+    float eps;
+    void* r_out;
+    void* x;
+    int64_t y_stride;
+    int64_t r_stride;
+    int64_t gate_stride;
+    int64_t r_out_stride;
+    int64_t x_stride;
+} qx_norm_args;
+qx_status qx_block_norm(const qx_norm_args* a, qx_stream_t s);
+
 /* Synchronise stream s, then read and clear the device error word of the
  * current device: QX_OK, QX_ERR_DEVICE_TIMEOUT if a kernel's bounded wait ran
- * out since the last check, or QX_ERR_CUDA if the synchronisation failed. */
+ * out since the last check, QX_ERR_RANGE if a kernel met a page, length or
+ * position out of range, or QX_ERR_CUDA if the synchronisation failed. */
 qx_status qx_device_check(qx_stream_t s);
 
 /* Static, NUL-terminated strings. */
