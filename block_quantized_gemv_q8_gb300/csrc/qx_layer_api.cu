@@ -65,7 +65,7 @@ qx_status attention(const qx_kv* kv, const void* q, int64_t n_tokens, int n_q_he
     if (n_tokens < 0 || n_tokens > INT32_MAX / 2) return QX_ERR_SHAPE;
     if (n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % kv->n_heads || n_q_heads / kv->n_heads > QX_MAX_GROUP)
         return QX_ERR_SHAPE;
-    if (!stride_ok(q_stride)) return QX_ERR_SHAPE;
+    if (!stride_ok(q_stride) || n_tokens * n_q_heads > INT32_MAX) return QX_ERR_SHAPE;
     if (window < 0 || sinks < 0 || shared_len < 0 || !std::isfinite(scale)) return QX_ERR_ARG;
     if (out_dtype != QX_F32 && out_dtype != kv->dtype) return QX_ERR_FMT;
     if (n_tokens == 0) return QX_OK;
@@ -149,7 +149,7 @@ size_t qx_attn_scratch_bytes(int64_t n_tokens, int n_q_heads, int n_heads, int h
         n_q_heads > 65535 || n_q_heads % n_heads || n_q_heads / n_heads > QX_MAX_GROUP || head_dim < 8 ||
         head_dim % 8 || head_dim > QX_MAX_HEAD_DIM || n_seqs < 1)
         return 0;
-    return 256;
+    return attn_scratch_bytes(n_tokens, n_q_heads, n_heads, head_dim, n_seqs);
 }
 
 qx_status qx_block_norm(const qx_norm_args* a, qx_stream_t s) {
