@@ -6,6 +6,7 @@
 // turns (m, l, o) into (M, l e^(m-M) + sum e^(s_j-M), o e^(m-M) + ...), M =
 // max(m, m'); the output is o / l.  Exponents are taken to base 2 with
 // scale * log2(e) folded into the scores.
+#include "qx_attn.cuh"
 #include "qx_layer.cuh"
 
 namespace qx {
@@ -181,12 +182,6 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uin
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float exp2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // What a sequence brings: its tokens, and the keys that any of them sees --
 // the first `sinks` (only where the window of the first token begins later)
 // and [lo, end) -- as units of 64: those of the sinks, then those from the
@@ -252,8 +247,13 @@ __device__ __forceinline__ int64_t unit_keys(const SeqWork& w, int u, int64_t& l
     return (w.lo / kUnit + (u - w.sink_units)) * kUnit;
 }
 
+struct SplitParams : AttnParams {
+    float* part_o;    // not null: the rows are a part to be joined (o / l, base-2 log of the sum)
+    float* part_lse;
+};
+
 template <typename T, int DIM>
-__global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __grid_constant__ SplitParams p) {
     using G = SplitGeom<DIM>;
     constexpr int KS = DIM / 16;  // 16-wide steps along a head
     extern __shared__ __align__(128) uint8_t smem[];
@@ -527,6 +527,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
             const int rr = kRows * cur.rt + r;
             const int64_t row = int64_t(cur.w.t0 + rr / group) * p.n_q_heads + cur.hk * group + rr % group;
             const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+            if (p.part_o) {
+                *reinterpret_cast<float2*>(p.part_o + row * DIM + d) = make_float2(x * inv, y * inv);
+                if (d == 0) p.part_lse[row] = L > 0.0f ? M + log2f(L) : -INFINITY;
+                return;
+            }
             if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + row * DIM + d) = make_float2(x * inv, y * inv);
             else *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * DIM + d) = pack2<T>(x * inv, y * inv);
             if (p.lse && d == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
@@ -592,7 +597,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
 }
 
 template <typename T, int DIM>
-cudaError_t launch_split(const AttnParams& p, int sm_count, cudaStream_t s) {
+cudaError_t launch_split(const SplitParams& p, int sm_count, cudaStream_t s) {
     static bool ready[64] = {false};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -607,26 +612,86 @@ cudaError_t launch_split(const AttnParams& p, int sm_count, cudaStream_t s) {
     return launch_serial(attn_split_kernel<T, DIM>, dim3(unsigned(workers)), kSplitThreads, SplitGeom<DIM>::kSmem, s, p);
 }
 
+cudaError_t launch_split_any(int dtype, const AttnParams& a, float* part_o, float* part_lse, int sm_count, cudaStream_t s) {
+    SplitParams p;
+    static_cast<AttnParams&>(p) = a;
+    p.part_o = part_o;
+    p.part_lse = part_lse;
+    const bool f16 = dtype == QX_F16;
+    if (a.kv.head_dim == 128)
+        return f16 ? launch_split<__half, 128>(p, sm_count, s) : launch_split<__nv_bfloat16, 128>(p, sm_count, s);
+    return f16 ? launch_split<__half, 64>(p, sm_count, s) : launch_split<__nv_bfloat16, 64>(p, sm_count, s);
+}
+
 template <typename T>
 cudaError_t launch_row(const AttnParams& p, cudaStream_t s) {
     return launch_serial(attn_row_kernel<T>, dim3(unsigned(p.n_tokens), unsigned(p.n_q_heads)), 32 * kRowWarps, 0, s, p);
 }
 
+constexpr size_t kSplitScratch = kCounterBytes + size_t(kMaxWorkers) * 2 * partial_floats<128>() * 4;
+// Rows of parts that the scratch holds: enough to split the keys of few rows
+// over the GPU, and two parts of any call whose shared prefix is taken apart.
+constexpr int64_t kPartRows = 65536, kMaxSharedRows = 131072;
+int64_t part_rows(int64_t rows) {
+    const int64_t two = 2 * (rows < kMaxSharedRows ? rows : kMaxSharedRows);
+    return two > kPartRows ? (two + 63) / 64 * 64 : kPartRows;  // 256-byte multiples
+}
+constexpr int kMaxSplits = 31;  // of one launch: with the tails' part a row has at most 32
+
+// CTAs that share a tile pair's keys: as many as give every SM one.
+int splits_for(int64_t ctas, int64_t rows, int64_t spare_rows, int sm_count) {
+    int64_t n = ctas > 0 ? sm_count / ctas : 1;
+    if (n > kMaxSplits) n = kMaxSplits;
+    if (n * rows > spare_rows) n = spare_rows / rows;
+    return n < 1 ? 1 : int(n);
+}
+
 }  // namespace
 
-size_t attn_scratch_bytes(int64_t, int, int, int, int) {
-    return kCounterBytes + size_t(kMaxWorkers) * 2 * partial_floats<128>() * 4;
+size_t attn_scratch_bytes(int64_t n_tokens, int n_q_heads, int, int head_dim, int) {
+    const int64_t rows = n_tokens * n_q_heads;
+    return kSplitScratch + (head_dim == 64 || head_dim == 128 ? size_t(part_rows(rows)) * (head_dim + 1) * 4 : 0);
 }
 
 cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaStream_t s) {
     AttnParams p = params;
-    p.shared_len = 0;
-    const bool f16 = dtype == QX_F16;
-    if (p.kv.head_dim == 128)
-        return f16 ? launch_split<__half, 128>(p, sm_count, s) : launch_split<__nv_bfloat16, 128>(p, sm_count, s);
-    if (p.kv.head_dim == 64)
-        return f16 ? launch_split<__half, 64>(p, sm_count, s) : launch_split<__nv_bfloat16, 64>(p, sm_count, s);
-    return f16 ? launch_row<__half>(p, s) : launch_row<__nv_bfloat16>(p, s);
+    const int dim = p.kv.head_dim;
+    if (dim != 64 && dim != 128) {
+        p.shared_len = 0;  // every sequence's table leads to the prefix, too
+        return dtype == QX_F16 ? launch_row<__half>(p, s) : launch_row<__nv_bfloat16>(p, s);
+    }
+    const int group = p.n_q_heads / p.kv.n_heads;
+    const int64_t rows = int64_t(p.n_tokens) * p.n_q_heads;
+    float* part_lse = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + kSplitScratch);
+    float* part_o = part_lse + part_rows(rows);
+    if (rows > kMaxSharedRows || p.n_tokens < 2) p.shared_len = 0;
+    // Rows of a key head a sequence, on average: the split kernel reads a
+    // sequence's keys once for every 16 of them, the tensor cores' once for
+    // 256, but only they need whole tiles to be efficient.
+    const bool many = int64_t(p.n_tokens) * group >= 64 * int64_t(p.kv.n_seqs);
+    JoinParams j;
+    j.a = p;
+    j.part_o = part_o;
+    j.part_lse = part_lse;
+    j.parts = 0;
+    cudaError_t e;
+    int64_t spare = part_rows(rows);
+    if (p.shared_len > 0) {
+        spare -= rows;  // the tails' part
+        j.parts = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, true) * p.kv.n_heads, rows, spare, sm_count);
+        if ((e = launch_attn_tc(dtype, p, true, j.parts, part_o, part_lse, s)) != cudaSuccess) return e;
+        float* o = part_o + j.parts * rows * dim;
+        float* l = part_lse + j.parts * rows;
+        ++j.parts;
+        e = many ? launch_attn_tc(dtype, p, false, 1, o, l, s) : launch_split_any(dtype, p, o, l, sm_count, s);
+        return e != cudaSuccess ? e : launch_attn_join(dtype, j, s);
+    }
+    if (!many) return launch_split_any(dtype, p, nullptr, nullptr, sm_count, s);
+    const int n = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, false) * p.kv.n_heads, rows, spare, sm_count);
+    if (n == 1) return launch_attn_tc(dtype, p, false, 1, nullptr, nullptr, s);
+    if ((e = launch_attn_tc(dtype, p, false, n, part_o, part_lse, s)) != cudaSuccess) return e;
+    j.parts = n;
+    return launch_attn_join(dtype, j, s);
 }
 
 }  // namespace qx

@@ -1,0 +1,40 @@
+// qx_attn.cuh -- what the attention kernels share (qx_attn.cu, qx_attn_tc.cu).
+#pragma once
+
+#include "qx_layer.cuh"
+
+namespace qx {
+
+template <typename T>
+struct IsBf16 {
+    static constexpr bool value = false;
+};
+template <>
+struct IsBf16<__nv_bfloat16> {
+    static constexpr bool value = true;
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Parts of every row, from calls that each saw some of its keys: o / l and
+// the base-2 log of the sum, [parts][tokens * heads] (at most 32 parts).
+struct JoinParams {
+    AttnParams a;
+    const float* part_o;
+    const float* part_lse;
+    int parts;
+};
+
+int64_t tc_pairs(int64_t n_tokens, int group, int n_seqs, bool prefix);
+// The tokens' attention on the tensor cores: over all their keys (from
+// shared_len on), or, `prefix`, over keys [0, shared_len) of the first
+// sequence.  part_o null: written to the output (one split).
+cudaError_t launch_attn_tc(int dtype, const AttnParams& a, bool prefix, int splits, float* part_o, float* part_lse,
+                           cudaStream_t s);
+cudaError_t launch_attn_join(int dtype, const JoinParams& p, cudaStream_t s);
+
+}  // namespace qx
