@@ -141,10 +141,10 @@ struct SplitGeom {
     static constexpr size_t kSmem = kRingBytes + kJoin;
 };
 
-// Scratch: arrival counters (one a worker, zero between calls), then two
-// partial tiles a worker: o [16][DIM], then m and l of the 16 rows.
+// Scratch: arrival counters (one a worker, and 64 words for the tensor-core
+// kernel's; zero between calls), then two partial tiles a worker: o [16][DIM], then m and l of the 16 rows.
 constexpr int kMaxWorkers = 512;
-constexpr size_t kCounterBytes = kMaxWorkers * 4;
+constexpr size_t kCounterBytes = (kMaxWorkers + 64) * 4;
 template <int DIM>
 __host__ __device__ constexpr int partial_floats() { return kRows * DIM + 2 * kRows; }
 
@@ -664,11 +664,13 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
     const int64_t rows = int64_t(p.n_tokens) * p.n_q_heads;
     float* part_lse = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + kSplitScratch);
     float* part_o = part_lse + part_rows(rows);
-    if (rows > kMaxSharedRows || p.n_tokens < 2) p.shared_len = 0;
+    // a scale that is not positive is an oddity that only the split kernel serves
+    unsigned* counter = static_cast<unsigned*>(p.scratch) + kMaxWorkers;
+    if (rows > kMaxSharedRows || p.n_tokens < 2 || p.scale_log2 <= 0.0f) p.shared_len = 0;
     // Rows of a key head a sequence, on average: the split kernel reads a
     // sequence's keys once for every 16 of them, the tensor cores' once for
     // 256, but only they need whole tiles to be efficient.
-    const bool many = int64_t(p.n_tokens) * group >= 64 * int64_t(p.kv.n_seqs);
+    const bool many = int64_t(p.n_tokens) * group >= 64 * int64_t(p.kv.n_seqs) && p.scale_log2 > 0.0f;
     JoinParams j;
     j.a = p;
     j.part_o = part_o;
@@ -679,17 +681,17 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
     if (p.shared_len > 0) {
         spare -= rows;  // the tails' part
         j.parts = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, true) * p.kv.n_heads, rows, spare, sm_count);
-        if ((e = launch_attn_tc(dtype, p, true, j.parts, part_o, part_lse, s)) != cudaSuccess) return e;
+        if ((e = launch_attn_tc(dtype, p, true, j.parts, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
         float* o = part_o + j.parts * rows * dim;
         float* l = part_lse + j.parts * rows;
         ++j.parts;
-        e = many ? launch_attn_tc(dtype, p, false, 1, o, l, s) : launch_split_any(dtype, p, o, l, sm_count, s);
+        e = many ? launch_attn_tc(dtype, p, false, 1, o, l, counter, sm_count, s) : launch_split_any(dtype, p, o, l, sm_count, s);
         return e != cudaSuccess ? e : launch_attn_join(dtype, j, s);
     }
     if (!many) return launch_split_any(dtype, p, nullptr, nullptr, sm_count, s);
     const int n = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, false) * p.kv.n_heads, rows, spare, sm_count);
-    if (n == 1) return launch_attn_tc(dtype, p, false, 1, nullptr, nullptr, s);
-    if ((e = launch_attn_tc(dtype, p, false, n, part_o, part_lse, s)) != cudaSuccess) return e;
+    if (n == 1) return launch_attn_tc(dtype, p, false, 1, nullptr, nullptr, counter, sm_count, s);
+    if ((e = launch_attn_tc(dtype, p, false, n, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
     j.parts = n;
     return launch_attn_join(dtype, j, s);
 }

@@ -21,6 +21,11 @@
 // against 128 x 128 exponentials: the tensor cores and the softmax warps take
 // about the same time, and which of them bounds depends on the head size.
 //
+// The CTAs are persistent (one an SM) and take tile pairs from a counter, those
+// with the most keys first.  A third warpgroup serves the two: a producer, which
+// takes the pairs and runs ahead with the copies, a warp that issues the MMAs, and a warp that zeroes values that no row sees.  The
+// next pair's first scores are computed during this pair's epilogue.
+//
 // A row's keys may be split over several CTAs (few rows, long context); each
 // part then leaves o / l and the base-2 log of its sum, which
 // attn_join_kernel joins.  Every wait is bounded and reports through the
@@ -41,8 +46,8 @@ namespace {
 constexpr int kKeys = 128;             // keys of a block
 constexpr int kTileRows = 128;         // rows of a tile; two tiles a CTA
 constexpr int kSoftmaxWarps = 8;       // two warpgroups
-// A third warpgroup: the MMA issuer, the producer, and two warps that only
-// give up registers.  An SM partition holds three of the CTA's warps, so 168
+// A third warpgroup: the MMA issuer, the producer, the warp that zeroes, and one
+// that only gives up registers.  An SM partition holds three of the CTA's warps, so 168
 // registers a thread at launch; the softmax warps hold a row of S each.
 constexpr int kTcThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -56,7 +61,7 @@ struct TcGeom {
     static constexpr int kPanelBytes = 128 * 128;               // 128 rows
     static constexpr int kTileBytes = kPanels * kPanelBytes;    // Q of a tile, or a block's K or V
     static constexpr int kSlots = DIM == 128 ? 5 : 10;          // ring of K and V blocks
-    static constexpr size_t kSmem = size_t(2 + kSlots) * kTileBytes + 1024 + 256;
+    static constexpr size_t kSmem = size_t(2 + kSlots) * kTileBytes + 1024 + 512;
 };
 static_assert(TcGeom<128>::kSmem <= 227 * 1024 && TcGeom<64>::kSmem <= 227 * 1024, "a CTA's shared memory");
 
@@ -70,6 +75,7 @@ struct TcAttnParams {
     int prefix;         // 1: every token against keys [0, shared_len)
     float* part_o;      // parts: [splits][tokens * heads][dim], or null: write the output
     float* part_lse;    // [splits][tokens * heads]
+    unsigned* counter;  // pairs taken beyond each CTA's first, and CTAs done; zero between calls
 };
 
 // Shared-memory matrix descriptors, 128-byte swizzle.  K-major: rows of 128
@@ -120,20 +126,36 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(id), "r"(acc)
         : "memory");
 }
+// One lane of a converged warp.  Around it the warp's code stays uniform, so
+// descriptors and tensor-memory addresses live in uniform registers; issued
+// from a lane-0 branch every MMA first had its operands moved there (75 to 90
+// cycles each, against 64 for the product itself).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+    return e != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
 }
 // 32 columns of the warp's 32 rows, no wait.
-__device__ __forceinline__ void ld32(uint32_t taddr, float* r) {
-    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+__device__ __forceinline__ void ld32(uint32_t taddr, float* u) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
-          "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
-          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3]), "=f"(u[4]), "=f"(u[5]), "=f"(u[6]), "=f"(u[7]), "=f"(u[8]),
+          "=f"(u[9]), "=f"(u[10]), "=f"(u[11]), "=f"(u[12]), "=f"(u[13]), "=f"(u[14]), "=f"(u[15]), "=f"(u[16]),
+          "=f"(u[17]), "=f"(u[18]), "=f"(u[19]), "=f"(u[20]), "=f"(u[21]), "=f"(u[22]), "=f"(u[23]), "=f"(u[24]),
+          "=f"(u[25]), "=f"(u[26]), "=f"(u[27]), "=f"(u[28]), "=f"(u[29]), "=f"(u[30]), "=f"(u[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void ld16(uint32_t taddr, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(taddr));
 }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -145,16 +167,16 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&u)[16]) {
         "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
         : "memory");
 }
-__device__ __forceinline__ void st32(uint32_t taddr, const float* r) {
-    const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
-        "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
-        "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
-        : "memory");
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Bits n .. 31 (all of them for n <= 0, none for n >= 32: the shift clamps).
+__device__ __forceinline__ uint32_t bits_from(int n) {
+    uint32_t r;
+    asm("shl.b32 %0, -1, %1;" : "=r"(r) : "r"(n > 0 ? n : 0));
+    return r;
 }
 
 // What a CTA works on: `tokens` tokens from t0 on (at most two tiles) of
@@ -162,6 +184,7 @@ __device__ __forceinline__ void st32(uint32_t taddr, const float* r) {
 // rows sees: those of keys [0, sinks), then those of [lo, end).
 struct TcWork {
     int b, t0, tokens, pos0, lo, end, sinks, sink_blocks, blocks;
+    int hk, split, i0, nb;  // key head, part, and its blocks [i0, i0 + nb)
 };
 __device__ __forceinline__ int key_block(const TcWork& w, int i) {  // first key of the i-th block
     return (i < w.sink_blocks ? i : w.lo / kKeys + (i - w.sink_blocks)) * kKeys;
@@ -241,6 +264,40 @@ __device__ __forceinline__ bool find_pair(const TcAttnParams& p, int number, int
     return false;
 }
 
+__device__ __forceinline__ bool block_has_unseen(const TcWork& w, int i) {
+    int lo, hi;
+    key_range(w, i, lo, hi);
+    const int j0 = key_block(w, i);
+    return j0 < lo || j0 + kKeys > hi;
+}
+__device__ __forceinline__ int count_pairs(const TcAttnParams& p, int lane) {
+    const KvView& kv = p.a.kv;
+    const int pair = 2 * p.tile_tokens;
+    if (p.prefix) {
+        const int total = kv.q_start[kv.n_seqs] < p.a.n_tokens ? kv.q_start[kv.n_seqs] : p.a.n_tokens;
+        return (total + pair - 1) / pair;
+    }
+    int sum = 0;
+    for (int b = lane; b < kv.n_seqs; b += 32) {
+        const int t0 = kv.q_start[b], n = kv.q_start[b + 1] - t0;
+        if (n > 0 && t0 >= 0 && t0 + n <= p.a.n_tokens) sum += (n + pair - 1) / pair;
+    }
+    return __reduce_add_sync(0xffffffffu, sum);
+}
+
+// A place in the ring and the parity of its current use.
+struct RingPos {
+    int slot = 0;
+    uint32_t phase = 0;
+    template <int NS>
+    __device__ __forceinline__ void next() {
+        if (++slot == NS) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 // Every lane of the warp waits itself, and the outcome is warp-uniform.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned* err, unsigned code) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitNs, err, code));
@@ -253,40 +310,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     uint8_t* sq = smem;                        // [2 tiles][panels][128 rows][128 B]
-    uint8_t* ring = sq + 2 * G::kTileBytes;    // [NS] blocks: K0, V0, K1, V1, ...
+    uint8_t* ring = sq + 2 * G::kTileBytes;    // [NS] blocks: K0, V0, K1, V1, ... of pair after pair
     uint64_t* q_full = reinterpret_cast<uint64_t*>(ring + NS * G::kTileBytes);
-    uint64_t* kv_full = q_full + 1;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* kv_full = q_empty + 1;
     uint64_t* kv_empty = kv_full + NS;
-    uint64_t* s_full = kv_empty + NS;   // per tile
-    uint64_t* p_full = s_full + 2;
-    uint64_t* o_full = p_full + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
+    uint64_t* clean = kv_empty + NS;  // there, and what no row sees of its values is zeroed
+    uint64_t* s_full = clean + NS;    // per tile
+    uint64_t* p_full = s_full + 2;      // per tile and half of the block's keys
+    uint64_t* o_full = p_full + 4;
+    uint64_t* o_empty = o_full + 2;
+    uint64_t* w_full = o_empty + 2;     // per entry of `work`
+    uint64_t* w_empty = w_full + 2;
+    TcWork* work = reinterpret_cast<TcWork*>(w_empty + 2);  // [2]: pairs in hand; tokens 0: no more
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(work + 2);
+    static_assert((2 + 3 * NS + 2 + 4 + 2 + 2 + 2 + 2) * 8 + 2 * sizeof(TcWork) + 4 <= 512, "barriers and work entries");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_wait_prior_grid();
-    pdl_launch_dependents();
     const KvView& kv = p.a.kv;
-    const int hk = blockIdx.x % kv.n_heads;
-    TcWork w;
-    // the pairs with the most keys (the last of a sequence) first
-    const int number = int(gridDim.x / kv.n_heads) - 1 - int(blockIdx.x / kv.n_heads);
-    if (!find_pair(p, number, lane, w)) return;
-    const int i0 = int(int64_t(w.blocks) * int(blockIdx.y) / p.splits);
-    const int i1 = int(int64_t(w.blocks) * (int(blockIdx.y) + 1) / p.splits);
-    const int nb = i1 - i0;  // this CTA's blocks
     const int group = p.a.n_q_heads / kv.n_heads;
-    const int tiles = w.tokens > p.tile_tokens ? 2 : 1;
-
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         for (int i = 0; i < NS; ++i) {
             mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
+            mbar_init(&clean[i], 1);
+            mbar_init(&kv_empty[i], 2);  // the MMAs that read it, and the warp that zeroes
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[2 * i], 4);
+            mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_full[i], 1);
+            mbar_init(&o_empty[i], 4);
+            mbar_init(&w_full[i], 1);
+            mbar_init(&w_empty[i], kSoftmaxWarps + 2);
         }
         fence_barrier_init();
     }
@@ -300,246 +358,371 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     tc_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem, tO = tmem + 256;  // S (and P) of tile t at 128 t, O at 256 + 128 t
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
 
-    if (warp >= kSoftmaxWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    if (warp == kSoftmaxWarps + 1) {
-        // ---- producer: Q, then K and V of each block
-        const int page_keys = (1 << kv.page_shift) < kKeys ? (1 << kv.page_shift) : kKeys;
-        const int boxes = kKeys / page_keys;  // of a block (at most 8)
-        if (nb > 0 && lane == 0) {
-            mbar_arrive_expect_tx(q_full, tiles * G::kPanels * p.tile_tokens * group * 128);
-            for (int t = 0; t < tiles; ++t)
-                for (int c = 0; c < G::kPanels; ++c)
-                    tma_3d(sq + t * G::kTileBytes + c * G::kPanelBytes, &p.q_map, 64 * c, hk * group, w.t0 + t * p.tile_tokens, q_full);
-        }
-        int issued = 0;
-        for (int i = 0; i < 2 * nb; ++i) {
-            const int slot = i % NS;
-            // lane x of the first `boxes` finds the page of its box
-            const int j0 = key_block(w, i0 + (i >> 1));
-            int lo, hi;
-            key_range(w, i0 + (i >> 1), lo, hi);
-            int page = -1;
-            if (lane < boxes) {
-                const int j = j0 + lane * page_keys;
-                if (j + page_keys > lo && j < hi) page = page_of(kv, w.b, j);
-            }
-            const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
-            if (i >= NS && !warp_wait(&kv_empty[slot], ((i / NS) - 1) & 1, kv.err, kErrTimeoutEmpty)) break;
-            if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], __popc(live) * page_keys * 128 * G::kPanels);
-            __syncwarp();
-            if (page >= 0) {
-                const int in_page = (j0 + lane * page_keys) & ((1 << kv.page_shift) - 1);
-                uint8_t* dst = ring + slot * G::kTileBytes + lane * page_keys * 128;
-                for (int c = 0; c < G::kPanels; ++c)
-                    tma_4d(dst + c * G::kPanelBytes, (i & 1) ? &p.v_map : &p.k_map, 64 * c, in_page, hk, page, &kv_full[slot]);
-            }
-            issued = i + 1;
-        }
-        // keep the CTA alive until every copy it issued has landed
-        if (lane == 0) {
-            if (nb > 0) mbar_wait_bounded(q_full, 0, kWaitNs, kv.err, kErrTimeoutDrain);
-            for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
-                mbar_wait_bounded(&kv_full[i % NS], (i / NS) & 1, kWaitNs, kv.err, kErrTimeoutDrain);
-        }
-    } else if (warp == kSoftmaxWarps) {
-        // ---- MMA issuer (the whole warp waits; lane 0 issues)
-        bool ok = nb > 0 && warp_wait(q_full, 0, kv.err, kErrTimeoutMma);
-        const uint32_t qa = smem_addr(sq), ra = smem_addr(ring);
-        const auto scores = [&](int t, int i) {  // S of tile t against block i (its K is in ring position 2 i)
-            const uint32_t ka = ra + ((2 * i) % NS) * G::kTileBytes;
-            if (lane == 0) {
-#pragma unroll
-                for (int k = 0; k < DIM / 16; ++k) {
-                    const uint32_t off = (k >> 2) * G::kPanelBytes + (k & 3) * 32;
-                    mma_ss(tS + 128 * t, sw128_desc(qa + t * G::kTileBytes + off, 16), sw128_desc(ka + off, 16),
-                           idesc<T>(kKeys, false), k > 0 ? 1u : 0u);
+    if (warp >= kSoftmaxWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kSoftmaxWarps + 1) {
+            // ---- producer: the pairs, and of each Q, then K and V of its blocks
+            const int page_keys = (1 << kv.page_shift) < kKeys ? (1 << kv.page_shift) : kKeys;
+            const int boxes = kKeys / page_keys;  // of a block (at most 8)
+            const int pairs = count_pairs(p, lane);
+            RingPos at;
+            int64_t issued = 0;
+            bool ok = true;
+            int quse = 0;
+            for (int n = 0; ok; ++n) {
+                if (n >= 2 && !(ok = warp_wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, kv.err, kErrTimeoutEmpty))) break;
+                int item = int(blockIdx.x);
+                if (n > 0) {
+                    if (lane == 0) item = int(gridDim.x + atomicAdd(p.counter, 1u));
+                    item = __shfl_sync(0xffffffffu, item, 0);
                 }
-                commit(&s_full[t]);
-            }
-            __syncwarp();
-        };
-        if (ok) ok = warp_wait(&kv_full[0], 0, kv.err, kErrTimeoutMma);
-        if (ok) {
-            tc_after();
-            for (int t = 0; t < tiles; ++t) scores(t, 0);
-            if (lane == 0) commit(&kv_empty[0]);
-        }
-        for (int i = 0; i < nb && ok; ++i) {
-            const int vs = (2 * i + 1) % NS, ks = (2 * i + 2) % NS;
-            const uint32_t va = ra + vs * G::kTileBytes;
-            if (!(ok = warp_wait(&kv_full[vs], ((2 * i + 1) / NS) & 1, kv.err, kErrTimeoutMma))) break;
-            // Values that no row sees are zeroed: whatever the slots hold, 0 x it must be 0.
-            int lo, hi;
-            key_range(w, i0 + i, lo, hi);
-            const int j0 = key_block(w, i0 + i);
-            if (j0 < lo || j0 + kKeys > hi) {
-                for (int r = lane; r < kKeys; r += 32)
-                    if (j0 + r < lo || j0 + r >= hi)
-                        for (int c = 0; c < G::kPanels; ++c)
-#pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                *reinterpret_cast<uint4*>(ring + vs * G::kTileBytes + c * G::kPanelBytes + r * 128 + 16 * x) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            if (i + 1 < nb && !(ok = warp_wait(&kv_full[ks], ((2 * i + 2) / NS) & 1, kv.err, kErrTimeoutMma))) break;
-            for (int t = 0; t < tiles; ++t) {
-                if (!(ok = warp_wait(&p_full[t], i & 1, kv.err, kErrTimeoutMma))) break;
-                tc_after();
+                TcWork w;
+                const int number = item / (kv.n_heads * p.splits), rest = item - number * (kv.n_heads * p.splits);
+                // the pairs with the most keys (the last of a sequence) first
+                const bool more = number < pairs && find_pair(p, pairs - 1 - number, lane, w);
+                if (!more) w.tokens = 0;
+                w.hk = rest / p.splits;
+                w.split = rest - w.hk * p.splits;
+                w.i0 = more ? int(int64_t(w.blocks) * w.split / p.splits) : 0;
+                w.nb = more ? int(int64_t(w.blocks) * (w.split + 1) / p.splits) - w.i0 : 0;
                 if (lane == 0) {
-#pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        mma_ts(tO + 128 * t, tS + 128 * t + 8 * k, sw128_desc(va + k * 2048, G::kPanelBytes), idesc<T>(DIM, true),
-                               (i | k) > 0 ? 1u : 0u);
-                    commit(&o_full[t]);
+                    work[n & 1] = w;
+                    mbar_arrive(&w_full[n & 1]);
+                }
+                if (!more) break;
+                if (w.nb == 0) continue;
+                const int tiles = w.tokens > p.tile_tokens ? 2 : 1;
+                if (quse > 0 && !(ok = warp_wait(q_empty, (quse - 1) & 1, kv.err, kErrTimeoutEmpty))) break;
+                ++quse;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, tiles * G::kPanels * p.tile_tokens * group * 128);
+                    for (int t = 0; t < tiles; ++t)
+                        for (int c = 0; c < G::kPanels; ++c)
+                            tma_3d(sq + t * G::kTileBytes + c * G::kPanelBytes, &p.q_map, 64 * c, w.hk * group,
+                                   w.t0 + t * p.tile_tokens, q_full);
                 }
                 __syncwarp();
-                if (i + 1 < nb) scores(t, i + 1);
+                // lane x of the first `boxes` finds the page of its box of the block, one block ahead
+                const auto page_of_box = [&](int i) -> int {
+                    int lo, hi;
+                    key_range(w, i, lo, hi);
+                    const int j = key_block(w, i) + lane * page_keys;
+                    return lane < boxes && j + page_keys > lo && j < hi ? page_of(kv, w.b, j) : -1;
+                };
+                int next_page = page_of_box(w.i0);
+                for (int i = w.i0; i < w.i0 + w.nb && ok; ++i) {
+                    const int page = next_page;
+                    if (i + 1 < w.i0 + w.nb) next_page = page_of_box(i + 1);
+                    const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
+                    const int in_page = (key_block(w, i) + lane * page_keys) & ((1 << kv.page_shift) - 1);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        if (issued >= NS && !(ok = warp_wait(&kv_empty[at.slot], at.phase ^ 1, kv.err, kErrTimeoutEmpty))) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&kv_full[at.slot], __popc(live) * page_keys * 128 * G::kPanels);
+                        __syncwarp();
+                        if (page >= 0) {
+                            uint8_t* dst = ring + at.slot * G::kTileBytes + lane * page_keys * 128;
+                            for (int c = 0; c < G::kPanels; ++c)
+                                tma_4d(dst + c * G::kPanelBytes, v ? &p.v_map : &p.k_map, 64 * c, in_page, w.hk, page,
+                                       &kv_full[at.slot]);
+                        }
+                        ++issued;
+                        at.template next<NS>();
+                    }
+                }
             }
-            if (ok && lane == 0) {
-                commit(&kv_empty[vs]);
-                if (i + 1 < nb) commit(&kv_empty[ks]);
+            // keep the CTA alive until every copy it issued has landed
+            if (lane == 0) {
+                if (quse > 0) mbar_wait_bounded(q_full, (quse - 1) & 1, kWaitNs, kv.err, kErrTimeoutDrain);
+                for (int64_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
+                    mbar_wait_bounded(&kv_full[i % NS], (i / NS) & 1, kWaitNs, kv.err, kErrTimeoutDrain);
             }
-            __syncwarp();
+        } else if (warp == kSoftmaxWarps) {
+            // ---- MMA issuer
+            const uint32_t base = uniform(smem_addr(sq)), tm = uniform(tmem);
+            const uint64_t q_desc = sw128_desc(base, 16), k_desc = sw128_desc(base + 2 * G::kTileBytes, 16),
+                           v_desc = sw128_desc(base + 2 * G::kTileBytes, G::kPanelBytes);
+            RingPos at;
+            uint32_t blocks[2] = {0, 0}, quse = 0;  // blocks of each tile, and pairs so far
+            bool ok = true;
+            const auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = warp_wait(bar, parity & 1, kv.err, kErrTimeoutMma);
+                return ok;
+            };
+            const auto wait2 = [&](uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
+                const bool first = mbar_try_wait(a, pa), second = mbar_try_wait(b, pb);
+                if (__all_sync(0xffffffffu, first && second)) return true;
+                return wait(a, pa) && wait(b, pb);
+            };
+            const auto scores = [&](int t, int slot, uint64_t* frees, uint64_t* frees_too) {
+                const uint64_t q = q_desc + t * (G::kTileBytes >> 4), k = k_desc + slot * (G::kTileBytes >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int x = 0; x < DIM / 16; ++x) {
+                        const uint64_t off = ((x >> 2) * G::kPanelBytes + (x & 3) * 32) >> 4;
+                        mma_ss(tm + 128 * t, q + off, k + off, idesc<T>(kKeys, false), x > 0 ? 1u : 0u);
+                    }
+                    commit(&s_full[t]);
+                    if (frees) commit(frees);
+                    if (frees_too) commit(frees_too);
+                }
+                __syncwarp();
+            };
+            const auto release = [&](uint64_t* bar, uint64_t* too) {
+                if (elect_one()) {
+                    commit(bar);
+                    if (too) commit(too);
+                }
+                __syncwarp();
+            };
+            for (int n = 0; ok; ++n) {
+                if (!wait(&w_full[n & 1], n >> 1)) break;
+                const TcWork w = work[n & 1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&w_empty[n & 1]);
+                const int tokens = int(uniform(uint32_t(w.tokens))), nb = int(uniform(uint32_t(w.nb)));
+                if (tokens == 0) break;
+                if (nb == 0) continue;
+                const int tiles = tokens > p.tile_tokens ? 2 : 1;
+                if (!wait(q_full, quse)) break;
+                if (!wait(&clean[at.slot], at.phase)) break;
+                tc_after();
+                for (int t = 0; t < tiles; ++t) scores(t, at.slot, nullptr, nullptr);
+                release(&kv_empty[at.slot], nb == 1 ? q_empty : nullptr);
+                at.template next<NS>();
+                RingPos v = at, k = at;  // the values of this block, the keys of the next
+                k.template next<NS>();
+                if (!wait(&clean[v.slot], v.phase) || (nb > 1 && !wait(&clean[k.slot], k.phase))) break;
+                for (int i = 0; i < nb && ok; ++i) {
+                    const bool last = i + 1 == nb;
+                    const uint64_t vd = v_desc + v.slot * (G::kTileBytes >> 4);
+                    const int v_slot = v.slot, k_slot = k.slot;
+                    for (int t = 0; t < tiles && ok; ++t) {
+                        // the pair before has left O
+                        if (i == 0 && quse > 0 && !wait(&o_empty[t], quse - 1)) break;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!wait(&p_full[2 * t + h], blocks[t])) break;
+                            tc_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int x = 4 * h; x < 4 * h + 4; ++x)
+                                    mma_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * x, vd + x * (2048 >> 4), idesc<T>(DIM, true),
+                                           (i | x) > 0 ? 1u : 0u);
+                                if (h == 1) {
+                                    commit(&o_full[t]);
+                                    if (t + 1 == tiles) commit(&kv_empty[v_slot]);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        ++blocks[t];
+                        if (last) continue;
+                        // while the pipe works: the next block's values and the keys after them
+                        if (t + 1 == tiles) {
+                            v = k;
+                            v.template next<NS>();
+                            k = v;
+                            k.template next<NS>();
+                            if (i + 2 < nb ? !wait2(&clean[v.slot], v.phase, &clean[k.slot], k.phase) : !wait(&clean[v.slot], v.phase)) break;
+                        }
+                        scores(t, k_slot, t + 1 == tiles ? &kv_empty[k_slot] : nullptr, t + 1 == tiles && i + 2 == nb ? q_empty : nullptr);
+                    }
+                }
+                at = k;  // past the last block's values
+                ++quse;
+            }
+        } else if (warp == kSoftmaxWarps + 2) {
+            // ---- values that no row sees are zeroed: whatever the slots hold, 0 x it must be 0
+            RingPos at;
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                if (!(ok = warp_wait(&w_full[n & 1], (n >> 1) & 1, kv.err, kErrTimeoutFull))) break;
+                const TcWork w = work[n & 1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&w_empty[n & 1]);
+                if (w.tokens == 0) break;
+                for (int i = w.i0; i < w.i0 + w.nb && ok; ++i) {
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        if (!(ok = warp_wait(&kv_full[at.slot], at.phase, kv.err, kErrTimeoutFull))) break;
+                        if (v && block_has_unseen(w, i)) {
+                            int lo, hi;
+                            key_range(w, i, lo, hi);
+                            const int j0 = key_block(w, i);
+                            for (int r = lane; r < kKeys; r += 32)
+                                if (j0 + r < lo || j0 + r >= hi)
+                                    for (int c = 0; c < G::kPanels; ++c)
+#pragma unroll
+                                        for (int x = 0; x < 8; ++x)
+                                            *reinterpret_cast<uint4*>(ring + at.slot * G::kTileBytes + c * G::kPanelBytes + r * 128 + 16 * x) =
+                                                make_uint4(0u, 0u, 0u, 0u);
+                            fence_proxy_async_smem();
+                        }
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&clean[at.slot]);
+                            mbar_arrive(&kv_empty[at.slot]);
+                        }
+                        at.template next<NS>();
+                    }
+                }
+            }
         }
-    } else if (warp < kSoftmaxWarps) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ---- softmax: one thread a row
         const int t = warp >> 2;  // tile
         const int r = 32 * (warp & 3) + lane;
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
         const uint32_t sa = tS + 128 * t + lanes, oa = tO + 128 * t + lanes;
-        const int in_tile = r / group, tok = t * p.tile_tokens + in_tile;
-        const bool live = in_tile < p.tile_tokens && tok < w.tokens;
-        int pos = -1;
-        if (live) {
-            if (p.prefix) {
-                const int seq = seq_of_token(kv, w.t0 + tok);
-                pos = seq < 0 ? -1 : int(position_of(kv, seq, w.t0 + tok));
-            } else {
-                pos = w.pos0 + tok;
-            }
-        }
+        const int in_tile = r / group, head = r - in_tile * group, tok = t * p.tile_tokens + in_tile;
         const int window = p.a.window > 0 && p.a.window < INT32_MAX ? int(p.a.window) : INT32_MAX;
         const int sinks = p.a.sinks < INT32_MAX ? int(p.a.sinks) : INT32_MAX;
-        const int wlo = pos >= window ? pos - window + 1 : 0;  // first key of this row's window
-        float m = -INFINITY, l = 0.0f;
-        bool ok = t < tiles;
-        for (int i = 0; i < nb && ok; ++i) {
-            if (!(ok = warp_wait(&s_full[t], i & 1, kv.err, kErrTimeoutMma))) break;
-            tc_after();
-            float s[kKeys];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) ld32(sa + 32 * c, s + 32 * c);
-            wait_ld();
-            const int j0 = key_block(w, i0 + i);
-            int lo, hi;
-            key_range(w, i0 + i, lo, hi);
-            const bool sink = i0 + i < w.sink_blocks;
-            const int first = sink ? 0 : (wlo > lo ? wlo : lo), last = (pos < hi - 1 ? pos : hi - 1);  // the row sees [first, last]
-            if (__any_sync(0xffffffffu, first > j0 || last < j0 + kKeys - 1)) {
-                // and, in a window block, sinks that the tile's first row has in its window
-                const int a = first - j0, b = last - j0, c0 = lo - j0, c1 = sinks - j0;
-#pragma unroll
-                for (int x = 0; x < kKeys; ++x)
-                    if (!((x >= a || (x >= c0 && x < c1)) && x <= b)) s[x] = -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int x = 4; x < kKeys; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
-            // base-2 scores: the maximum of s scale is scale times the maximum, or the minimum for a negative scale
-            float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.a.scale_log2;
-            if (p.a.scale_log2 <= 0.0f) {
-                // a rare sign: scaled scores instead (masked ones stay at -inf)
-                top = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < kKeys; ++x) {
-                    s[x] = s[x] == -INFINITY ? -INFINITY : s[x] * p.a.scale_log2;
-                    top = fmaxf(top, s[x]);
-                }
-            }
-            const float f = p.a.scale_log2 <= 0.0f ? 1.0f : p.a.scale_log2;
-            if (__any_sync(0xffffffffu, top > m + kRescale || (m == -INFINITY && top > m))) {
-                const float mn = fmaxf(m, top);
-                const float a = mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
-                l *= a;
-                m = mn;
-                if (i > 0) {
-                    if (!(ok = warp_wait(&o_full[t], (i - 1) & 1, kv.err, kErrTimeoutMma))) break;
-                    tc_after();
-#pragma unroll
-                    for (int c = 0; c < DIM / 32; ++c) {
-                        float o[32];
-                        ld32(oa + 32 * c, o);
-                        wait_ld();
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] *= a;
-                        st32(oa + 32 * c, o);
-                    }
-                    wait_st();
-                }
-            }
-            const float base = m == -INFINITY ? 0.0f : m;
-            const uint64_t f2 = f32x2_pack(f, f), b2 = f32x2_pack(-base, -base);
-            uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t u[16];
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const float2 e = f32x2_unpack(f32x2_fma(f32x2_pack(s[32 * c + 2 * x], s[32 * c + 2 * x + 1]), f2, b2));
-                    const float e0 = exp2_approx(e.x), e1 = exp2_approx(e.y);
-                    sum[x & 1] = f32x2_add(sum[x & 1], f32x2_pack(e0, e1));
-                    u[x] = pack2<T>(e0, e1);
-                }
-                st16(sa + 16 * c, u);
-            }
-            const float2 s01 = f32x2_unpack(f32x2_add(sum[0], sum[1]));
-            l += s01.x + s01.y;
-            wait_st();
-            tc_before();
+        const float f = p.a.scale_log2;  // positive: the split kernel takes the others
+        uint32_t blocks = 0;             // of this tile so far
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            if (!(ok = warp_wait(&w_full[n & 1], (n >> 1) & 1, kv.err, kErrTimeoutMma))) break;
+            const TcWork w = work[n & 1];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[t]);
-        }
-        // ---- output
-        if (t < tiles && ok && nb > 0) {
-            ok = warp_wait(&o_full[t], (nb - 1) & 1, kv.err, kErrTimeoutMma);
-            tc_after();
-        }
-        if (t < tiles && ok) {
-            const int64_t row = int64_t(w.t0 + tok) * p.a.n_q_heads + hk * group + r % group;
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            const float lse2 = l > 0.0f ? m + log2f(l) : -INFINITY;
-            const int64_t part = int64_t(blockIdx.y) * p.a.n_tokens * p.a.n_q_heads + row;
+            if (lane == 0) mbar_arrive(&w_empty[n & 1]);
+            if (w.tokens == 0) break;
+            const int tiles = w.tokens > p.tile_tokens ? 2 : 1;
+            if (t >= tiles) {  // no rows for this warpgroup
+                if (w.nb > 0 && lane == 0) mbar_arrive(&o_empty[t]);
+                continue;
+            }
+            const bool live = in_tile < p.tile_tokens && tok < w.tokens;
+            int pos = -1;
             if (live) {
+                if (p.prefix) {
+                    const int seq = seq_of_token(kv, w.t0 + tok);
+                    pos = seq < 0 ? -1 : int(position_of(kv, seq, w.t0 + tok));
+                } else {
+                    pos = w.pos0 + tok;
+                }
+            }
+            const int wlo = pos >= window ? pos - window + 1 : 0;  // first key of this row's window
+            float m = -INFINITY, l = 0.0f;
+            float s[kKeys];
+            for (int i = 0; i < w.nb; ++i) {
+                if (!(ok = warp_wait(&s_full[t], blocks & 1, kv.err, kErrTimeoutMma))) break;
+                tc_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ld32(sa + 32 * c, s + 32 * c);
+                const int j0 = key_block(w, w.i0 + i);
+                int lo, hi;
+                key_range(w, w.i0 + i, lo, hi);
+                // the row sees [first, last] (a thread without a row: whatever does not make its warp mask)
+                const int first = !live || w.i0 + i < w.sink_blocks ? 0 : (wlo > lo ? wlo : lo);
+                const int last = !live ? INT32_MAX - 1 : pos < hi - 1 ? pos : hi - 1;
+                wait_ld();
+                if (__any_sync(0xffffffffu, first > j0 || last < j0 + kKeys - 1)) {
+                    // and, in a window block, sinks that the pair's first row has in its window
+                    const int a = first - j0, b = last - j0, c0 = lo - j0, c1 = sinks - j0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t see = (bits_from(a - 32 * k) | (bits_from(c0 - 32 * k) & ~bits_from(c1 - 32 * k))) &
+                                             ~bits_from(b + 1 - 32 * k);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (!(see & (1u << x))) s[32 * k + x] = -INFINITY;
+                    }
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int x = 4; x < kKeys; x += 8)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) mx[y] = x + 4 < kKeys ? max3(mx[y], s[x + y], s[x + 4 + y]) : fmaxf(mx[y], s[x + y]);
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * f;
+                if (__any_sync(0xffffffffu, top > m + kRescale)) {
+                    const float mn = fmaxf(m, top);
+                    const float a = mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
+                    l *= a;
+                    m = mn;
+                    if (i > 0) {
+                        if (!(ok = warp_wait(&o_full[t], (blocks - 1) & 1, kv.err, kErrTimeoutMma))) break;
+                        tc_after();
+#pragma unroll
+                        for (int c = 0; c < DIM / 16; ++c) {
+                            float o[16];
+                            ld16(oa + 16 * c, o);
+                            wait_ld();
+                            uint32_t u[16];
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(o[x] * a);
+                            st16(oa + 16 * c, u);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+                const uint64_t f2 = f32x2_pack(f, f), b2 = f32x2_pack(-base, -base);
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t u[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const float2 e = f32x2_unpack(f32x2_fma(f32x2_pack(s[32 * c + 2 * x], s[32 * c + 2 * x + 1]), f2, b2));
+                        const float e0 = exp2_approx(e.x), e1 = exp2_approx(e.y);
+                        sum[x & 1] = f32x2_add(sum[x & 1], f32x2_pack(e0, e1));
+                        u[x] = pack2<T>(e0, e1);
+                    }
+                    st16(sa + 16 * c, u);
+                    if (c & 1) {  // half of the keys: the tensor cores may begin
+                        wait_st();
+                        tc_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[2 * t + (c >> 1)]);
+                    }
+                }
+                const float2 s01 = f32x2_unpack(f32x2_add(sum[0], sum[1]));
+                l += s01.x + s01.y;
+                ++blocks;
+            }
+            if (!ok) break;
+            // ---- output
+            if (w.nb > 0) {
+                if (!(ok = warp_wait(&o_full[t], (blocks - 1) & 1, kv.err, kErrTimeoutMma))) break;
+                tc_after();
+#pragma unroll
+                for (int c = 0; c < DIM / 32; ++c) ld32(oa + 32 * c, s + 32 * c);
+                wait_ld();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_empty[t]);
+            }
+            if (live) {
+                const int64_t row = int64_t(w.t0 + tok) * p.a.n_q_heads + w.hk * group + head;
+                const float inv = 1.0f / l;
+                const float lse2 = l > 0.0f ? m + log2f(l) : -INFINITY;
+                const int64_t part = int64_t(w.split) * p.a.n_tokens * p.a.n_q_heads + row;
                 if (p.part_o) p.part_lse[part] = lse2;
                 else if (p.a.lse) p.a.lse[row] = lse2 * 0.6931471805599453f;
+    #pragma unroll
+                for (int x = 0; x < DIM; ++x) s[x] = l > 0.0f ? s[x] * inv : 0.0f;  // (l is 0 where there was no block)
+                if (p.part_o) store_f32<DIM>(p.part_o + part * DIM, reinterpret_cast<float(&)[DIM]>(s));
+                else if (p.a.out_f32) store_f32<DIM>(static_cast<float*>(p.a.out) + row * DIM, reinterpret_cast<float(&)[DIM]>(s));
+                else store_f32<DIM>(static_cast<T*>(p.a.out) + row * DIM, reinterpret_cast<float(&)[DIM]>(s));
             }
-#pragma unroll
-            for (int c = 0; c < DIM / 32; ++c) {
-                float o[32];
-                if (nb > 0) {
-                    ld32(oa + 32 * c, o);
-                    wait_ld();
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = l > 0.0f ? o[x] * inv : 0.0f;
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = 0.0f;
-                }
-                if (!live) continue;
-                if (p.part_o) store_f32<32>(p.part_o + part * DIM + 32 * c, o);
-                else if (p.a.out_f32) store_f32<32>(static_cast<float*>(p.a.out) + row * DIM + 32 * c, o);
-                else store_f32<32>(static_cast<T*>(p.a.out) + row * DIM + 32 * c, o);
-            }
+            __syncwarp();
         }
     }
     tc_before();
     __syncthreads();
+    __syncwarp();
     if (warp == kSoftmaxWarps)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    if (threadIdx.x == 0) {
+        // the last CTA leaves the counters at zero for the next call
+        __threadfence();
+        if (atomicAdd(p.counter + 1, 1u) == gridDim.x - 1) p.counter[0] = p.counter[1] = 0;
+    }
 }
 
 // Join the parts of a row: out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).
@@ -622,7 +805,8 @@ bool encode(CUtensorMap* m, bool f16, const void* ptr, int rank, const int64_t* 
 }
 
 template <typename T, int DIM>
-cudaError_t launch_tc(const AttnParams& a, bool prefix, int splits, float* part_o, float* part_lse, cudaStream_t s) {
+cudaError_t launch_tc(const AttnParams& a, bool prefix, int splits, float* part_o, float* part_lse, unsigned* counter,
+                      int sm_count, cudaStream_t s) {
     static bool ready[64] = {false};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -640,6 +824,7 @@ cudaError_t launch_tc(const AttnParams& a, bool prefix, int splits, float* part_
     p.splits = splits;
     p.part_o = part_o;
     p.part_lse = part_lse;
+    p.counter = counter;
     const int group = a.n_q_heads / a.kv.n_heads;
     p.tile_tokens = kTileRows / group;
     const int page = 1 << a.kv.page_shift;
@@ -652,8 +837,8 @@ cudaError_t launch_tc(const AttnParams& a, bool prefix, int splits, float* part_
     if (!encode(&p.k_map, f16, a.kv.k, 4, kd, ks, kb) || !encode(&p.v_map, f16, a.kv.v, 4, kd, ks, kb) ||
         !encode(&p.q_map, f16, a.q, 3, qd, qs, qb))
         return cudaErrorInvalidValue;
-    const int64_t pairs = tc_pairs(a.n_tokens, group, a.kv.n_seqs, prefix);
-    return launch_serial(attn_tc_kernel<T, DIM>, dim3(unsigned(pairs * a.kv.n_heads), unsigned(splits)), kTcThreads,
+    const int64_t items = tc_pairs(a.n_tokens, group, a.kv.n_seqs, prefix) * a.kv.n_heads * splits;
+    return launch_serial(attn_tc_kernel<T, DIM>, dim3(unsigned(items < sm_count ? items : sm_count)), kTcThreads,
                          TcGeom<DIM>::kSmem, s, p);
 }
 
@@ -666,12 +851,12 @@ int64_t tc_pairs(int64_t n_tokens, int group, int n_seqs, bool prefix) {
 }
 
 cudaError_t launch_attn_tc(int dtype, const AttnParams& a, bool prefix, int splits, float* part_o, float* part_lse,
-                           cudaStream_t s) {
+                           unsigned* counter, int sm_count, cudaStream_t s) {
     if (a.kv.head_dim == 128)
-        return dtype == QX_F16 ? launch_tc<__half, 128>(a, prefix, splits, part_o, part_lse, s)
-                               : launch_tc<__nv_bfloat16, 128>(a, prefix, splits, part_o, part_lse, s);
-    return dtype == QX_F16 ? launch_tc<__half, 64>(a, prefix, splits, part_o, part_lse, s)
-                           : launch_tc<__nv_bfloat16, 64>(a, prefix, splits, part_o, part_lse, s);
+        return dtype == QX_F16 ? launch_tc<__half, 128>(a, prefix, splits, part_o, part_lse, counter, sm_count, s)
+                               : launch_tc<__nv_bfloat16, 128>(a, prefix, splits, part_o, part_lse, counter, sm_count, s);
+    return dtype == QX_F16 ? launch_tc<__half, 64>(a, prefix, splits, part_o, part_lse, counter, sm_count, s)
+                           : launch_tc<__nv_bfloat16, 64>(a, prefix, splits, part_o, part_lse, counter, sm_count, s);
 }
 
 cudaError_t launch_attn_join(int dtype, const JoinParams& p, cudaStream_t s) {

@@ -112,6 +112,21 @@ def test_attention_shapes(heads, batch):
         b.check(out, lse, b.expect(dim ** -0.5, window, sinks), f"heads {heads} page {page} window {window} sinks {sinks}")
 
 
+@pytest.mark.parametrize("heads", [(32, 8, 128), (28, 4, 64)])
+@pytest.mark.parametrize("window,sinks", [(100, 4), (150, 200), (0, 0), (64, 0)])
+def test_prefill_of_more_tiles_than_the_gpu_holds(heads, window, sinks):
+    """Each SM takes several tile pairs one after another."""
+    hq, hkv, dim = heads
+    q_lens = [1700, 3, 900, 40] if window else [700, 300, 1, 500]
+    kv_lens = [1700, 90, 1500, 300] if window else [700, 400, 60, 500]
+    if not window:
+        hq, hkv = 8 * hkv * 4, 4 * hkv
+    b = Batch(q_lens, kv_lens, hq, hkv, dim, 16, BF16, seed=12)
+    lse = torch.empty((b.T, hq), device="cuda")
+    out = qx.qx_attn_paged(b.kv, b.q, window=window, sinks=sinks, lse=lse)
+    b.check(out, lse, b.expect(dim ** -0.5, window, sinks), f"{heads} window {window}")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("q_lens,kv_lens", [([1], [5000]), ([300], [2500]), ([1, 1, 200], [3000, 1, 900])])
 @pytest.mark.parametrize("std", [0.0, 1.0, 30.0])
