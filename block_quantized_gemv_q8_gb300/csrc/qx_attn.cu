@@ -136,9 +136,10 @@ struct SplitGeom {
     static constexpr int kRowBytes = 2 * DIM;
     static constexpr int kStageBytes = 2 * 16 * kRowBytes;  // one warp's keys and values
     static constexpr int kStages = kRingBytes / (kSplitWarps * kStageBytes);
-    static constexpr int kPad = DIM + 4;                     // floats of a row in the joining buffer
-    static constexpr int kJoin = 2 * kRows * (kPad + 2) * 4;
+    static constexpr int kPad = DIM + 4;  // floats of a row in the joining buffer: 8 rows of each warp, then their m and l
+    static constexpr int kJoin = (kSplitWarps * 8 * (kPad + 2)) * 4;
     static constexpr size_t kSmem = kRingBytes + kJoin;
+    static_assert(2 * (kSmem + 1200) <= 228 * 1024, "two CTAs an SM");
 };
 
 // Scratch: arrival counters (one a worker, and 64 words for the tensor-core
@@ -250,7 +251,14 @@ __device__ __forceinline__ int64_t unit_keys(const SeqWork& w, int u, int64_t& l
 struct SplitParams : AttnParams {
     float* part_o;    // not null: the rows are a part to be joined (o / l, base-2 log of the sum)
     float* part_lse;
+    int beside;       // 1: launched beside the kernel before it, which belongs to the same call
 };
+
+// Quotients of non-negative numbers, in 32 bits where they fit (nearly always).
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return int64_t(uint32_t(a) / uint32_t(b));
+    return a / b;
+}
 
 template <typename T, int DIM>
 __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __grid_constant__ SplitParams p) {
@@ -258,9 +266,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     constexpr int KS = DIM / 16;  // 16-wide steps along a head
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t scan[kSplitWarps];
-    __shared__ int64_t found_begin;
-    __shared__ int found_b, last_flag;
-    pdl_wait_prior_grid();
+    __shared__ Cursor start;
+    __shared__ int last_flag;
+    // Beside a kernel that works on the same call's prefix: that one has
+    // waited for the work before it, and this one reads nothing of its.
+    if (!p.beside) pdl_wait_prior_grid();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = p.n_q_heads / p.kv.n_heads;
@@ -269,9 +279,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     // ---- the line's length, and where this worker's share begins
     int64_t mine = 0;
     const int per = (B + kSplitThreads - 1) / kSplitThreads, b0 = threadIdx.x * per;
+    SeqWork own;  // of the thread's last sequence (its only one, for up to 128 sequences)
     for (int b = b0; b < b0 + per && b < B; ++b) {
-        const SeqWork w = seq_work(p, b, group, blockIdx.x == 0);
-        mine += int64_t(w.row_tiles) * p.kv.n_heads * w.units;
+        own = seq_work(p, b, group, blockIdx.x == 0);
+        mine += int64_t(own.row_tiles) * p.kv.n_heads * own.units;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -280,7 +291,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         if (lane >= o) incl += v;
     }
     if (lane == 31) scan[warp] = incl;
-    if (threadIdx.x == 0) found_b = -1;
     __syncthreads();
     int64_t U = 0, before = 0;
 #pragma unroll
@@ -289,32 +299,37 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         U += scan[w];
     }
     const int64_t N = gridDim.x < U ? gridDim.x : U;
-    if (blockIdx.x >= N) return;
-    const int64_t first = blockIdx.x * U / N, last = (blockIdx.x + 1) * U / N;  // this worker's units
+    if (blockIdx.x >= N) {
+        if (p.beside) pdl_wait_prior_grid();
+        return;
+    }
+    // the first `extra` workers have one unit more than the others
+    const int64_t share = quot(U, N), extra = U - share * N;
+    const auto begin_of = [&](int64_t w) { return w * share + (w < extra ? w : extra); };
+    const auto worker_of = [&](int64_t u) {
+        return u < extra * (share + 1) ? quot(u, share + 1) : extra + quot(u - extra * (share + 1), share);
+    };
+    const int64_t first = begin_of(blockIdx.x), last = begin_of(blockIdx.x + 1);  // this worker's units
     int64_t at = before + incl - mine;
     if (first >= at && first < at + mine) {
         for (int b = b0; b < b0 + per && b < B; ++b) {
-            const SeqWork w = seq_work(p, b, group, false);
-            const int64_t n = int64_t(w.row_tiles) * p.kv.n_heads * w.units;
+            if (per > 1) own = seq_work(p, b, group, false);
+            const int64_t n = int64_t(own.row_tiles) * p.kv.n_heads * own.units;
             if (first < at + n) {
-                found_b = b;
-                found_begin = at;
+                const int64_t tile = quot(first - at, own.units);
+                start.b = b;
+                start.w = own;
+                start.begin = at + tile * own.units;
+                start.rt = int(quot(tile, p.kv.n_heads));
+                start.hk = int(tile - int64_t(start.rt) * p.kv.n_heads);
                 break;
             }
             at += n;
         }
     }
     __syncthreads();
-    Cursor ld;  // of the unit being fetched
-    ld.b = found_b;
-    ld.w = seq_work(p, ld.b, group, false);
-    {
-        const int64_t tile = (first - found_begin) / ld.w.units;
-        ld.begin = found_begin + tile * ld.w.units;
-        ld.rt = int(tile / p.kv.n_heads);
-        ld.hk = int(tile % p.kv.n_heads);
-    }
-    Cursor cur = ld;  // of the unit being computed
+    Cursor ld = start;   // of the unit being fetched
+    Cursor cur = start;  // of the unit being computed
 
     // ---- this warp's ring
     uint8_t* ring = smem + warp * (G::kStages * G::kStageBytes);
@@ -361,30 +376,33 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     uint32_t qf[KS][4];
     float o[DIM / 8][4], m[2], l[2];
     int64_t rpos[2];  // positions of this lane's two rows (-1: none)
+    // A tile's rows: 16 rt + lane / 4 and eight further.
+    const auto open_tile = [&](const Cursor& c) {
+        const int rows = c.w.tokens * group;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = kRows * c.rt + (lane >> 2) + 8 * i;
+            const bool live = r < rows;
+            const int tok = live ? r / group : 0, g = live ? r - tok * group : 0;
+            rpos[i] = live ? c.w.pos0 + tok : -1;
+            const T* q = static_cast<const T*>(p.q) + int64_t(c.w.t0 + tok) * p.q_stride + int64_t(c.hk * group + g) * DIM + 2 * (lane & 3);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                qf[k][i] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
+                qf[k][i + 2] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
+            }
+        }
+    };
+    open_tile(cur);
     float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(p.scratch) + kCounterBytes);
     unsigned* counters = static_cast<unsigned*>(p.scratch);
+    float* buf = reinterpret_cast<float*>(smem + kRingBytes);  // [4 warps][8 rows][kPad], then m and l of each
+    float* buf_ml = buf + kSplitWarps * 8 * G::kPad;
     int stage = 0;
     for (int64_t u = first; u < last; ++u) {
-        const bool opens = u == first || u == cur.begin;
-        if (opens) {
-            // the tile's rows: 16 rt + lane / 4 and eight further
-            const int rows = cur.w.tokens * group;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = kRows * cur.rt + (lane >> 2) + 8 * i;
-                const bool live = r < rows;
-                const int tok = live ? r / group : 0, g = live ? r % group : 0;
-                rpos[i] = live ? cur.w.pos0 + tok : -1;
-                const T* q = static_cast<const T*>(p.q) + int64_t(cur.w.t0 + tok) * p.q_stride +
-                             int64_t(cur.hk * group + g) * DIM + 2 * (lane & 3);
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    qf[k][i] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
-                    qf[k][i + 2] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
-                }
-                m[i] = -INFINITY;
-                l[i] = 0.0f;
-            }
+        if (u == first || u == cur.begin) {
+            m[0] = m[1] = -INFINITY;
+            l[0] = l[1] = 0.0f;
 #pragma unroll
             for (int d = 0; d < DIM / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.0f;
         }
@@ -406,21 +424,30 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                     mma16816<T>(s[1], qf[k], b[2], b[3]);
                 }
             }
+            // This lane's keys relative to the sixteen's first: 2 (lane % 4) + {0, 1, 8, 9}.
             const bool sink_unit = u - cur.begin < cur.w.sink_units;
+            const int first_key = lo > j0 ? int(lo - j0) : 0, end_key = hi < j0 + 16 ? int(hi - j0) : 16;
             float mx[2] = {m[0], m[1]};
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int64_t j = j0 + 8 * n + 2 * (lane & 3) + (e & 1);
-                    const int64_t pos = rpos[e >> 1];
-                    const bool see = j >= lo && j < hi && j <= pos &&
-                                     (sink_unit || p.window == 0 || j > pos - p.window || j < p.sinks);
-                    s[n][e] = see ? s[n][e] * p.scale_log2 : -INFINITY;
-                    mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
+            for (int i = 0; i < 2; ++i) {
+                const int64_t back = rpos[i] - j0;  // the row's position among them
+                const int end = back < end_key - 1 ? int(back < -1 ? -1 : back) + 1 : end_key;
+                int from = first_key, sink_end = 0;
+                if (p.window > 0 && !sink_unit) {
+                    const int64_t f = back - p.window + 1;
+                    from = f > first_key ? (f < 16 ? int(f) : 16) : first_key;
+                    const int64_t e = p.sinks - j0;
+                    sink_end = e < 0 ? 0 : e < 16 ? int(e) : 16;
                 }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = 8 * n + 2 * (lane & 3) + e;
+                        const bool see = j < end && (j >= from || (j >= first_key && j < sink_end));
+                        s[n][2 * i + e] = see ? s[n][2 * i + e] * p.scale_log2 : -INFINITY;
+                        mx[i] = fmaxf(mx[i], s[n][2 * i + e]);
+                    }
                 mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
                 mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
             }
@@ -468,132 +495,130 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         }
         if (++stage == G::kStages) stage = 0;
 
-        const bool closes = u + 1 == last || u + 1 == cur.begin + cur.w.units;
-        if (!closes) continue;
-        // ---- the tile ends here (for this worker): join the four warps
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        }
-        float* buf = reinterpret_cast<float*>(smem + kRingBytes);
-        const auto give = [&](float* to) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = (lane >> 2) + 8 * i;
-                float* row = to + r * G::kPad + 2 * (lane & 3);
-#pragma unroll
-                for (int d = 0; d < DIM / 8; ++d)
-                    *reinterpret_cast<float2*>(row + 8 * d) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
-                if ((lane & 3) == 0) {
-                    to[kRows * G::kPad + r] = m[i];
-                    to[kRows * G::kPad + kRows + r] = l[i];
-                }
-            }
-        };
-        const auto take = [&](const float* from) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = (lane >> 2) + 8 * i;
-                const float om = from[kRows * G::kPad + r], ol = from[kRows * G::kPad + kRows + r];
-                const float M = fmaxf(m[i], om);
-                const float a = m[i] == -INFINITY ? 0.0f : exp2_approx(m[i] - M), c = om == -INFINITY ? 0.0f : exp2_approx(om - M);
-                m[i] = M;
-                l[i] = l[i] * a + ol * c;
-                const float* row = from + r * G::kPad + 2 * (lane & 3);
-#pragma unroll
-                for (int d = 0; d < DIM / 8; ++d) {
-                    const float2 v = *reinterpret_cast<const float2*>(row + 8 * d);
-                    o[d][2 * i] = o[d][2 * i] * a + v.x * c;
-                    o[d][2 * i + 1] = o[d][2 * i + 1] * a + v.y * c;
-                }
-            }
-        };
-        float* half0 = buf;
-        float* half1 = buf + kRows * (G::kPad + 2);
-        __syncthreads();
-        if (warp >= 2) give(warp == 2 ? half0 : half1);
-        __syncthreads();
-        if (warp < 2) take(warp == 0 ? half0 : half1);
-        __syncthreads();
-        if (warp == 1) give(half0);
-        __syncthreads();
-        if (warp == 0) take(half0);
-        // ---- write the tile, or this worker's part of it
-        const int rows = cur.w.tokens * group - kRows * cur.rt;  // of this tile (16 at most count)
         const int64_t t_end = cur.begin + cur.w.units;
-        const int64_t wf = ((cur.begin + 1) * N - 1) / U, wl = (t_end * N - 1) / U;  // the first and last worker of the tile
-        const auto finish = [&](int r, int d, float M, float L, float x, float y) {
-            const int rr = kRows * cur.rt + r;
-            const int64_t row = int64_t(cur.w.t0 + rr / group) * p.n_q_heads + cur.hk * group + rr % group;
+        if (u + 1 != last && u + 1 != t_end) continue;
+        // ---- the tile ends here (for this worker).  The next one's queries
+        // are on their way while its warps are joined, eight rows at a time:
+        // every warp leaves its (m, l, o), and every thread then joins some
+        // elements.
+        const Cursor done = cur;
+        if (u + 1 < last) {
+            next_tile(p, cur, group);
+            open_tile(cur);
+        }
+        const int rows = done.w.tokens * group - kRows * done.rt;  // of this tile (16 at most count)
+        const int64_t wf = worker_of(done.begin), wl = worker_of(t_end - 1);  // the first and last worker of the tile
+        // A worker's part of a tile lies in its first slot, or in its second
+        // where another tile's end came first.
+        const auto slot_of = [&](int64_t w) -> float* { return partials + 2 * w * partial_floats<DIM>(); };
+        float* const wf_slot = slot_of(wf) + (begin_of(wf) < done.begin ? partial_floats<DIM>() : 0);
+        const auto finish = [&](int r, int d, float M, float L, float4 v) {
+            const int rr = kRows * done.rt + r;
+            const int64_t row = int64_t(done.w.t0 + rr / group) * p.n_q_heads + done.hk * group + rr % group;
             const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
             if (p.part_o) {
-                *reinterpret_cast<float2*>(p.part_o + row * DIM + d) = make_float2(x * inv, y * inv);
+                *reinterpret_cast<float4*>(p.part_o + row * DIM + d) = v;
                 if (d == 0) p.part_lse[row] = L > 0.0f ? M + log2f(L) : -INFINITY;
                 return;
             }
-            if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + row * DIM + d) = make_float2(x * inv, y * inv);
-            else *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * DIM + d) = pack2<T>(x * inv, y * inv);
+            if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * DIM + d) = v;
+            else *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * DIM + d) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
             if (p.lse && d == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
         };
-        if (wf == wl) {
-            if (warp == 0) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = (lane >> 2) + 8 * i;
-                    if (r < rows)
+        for (int i = 0; i < 2; ++i) {
+            if (8 * i >= rows) break;
+            const int live = rows - 8 * i < 8 ? rows - 8 * i : 8;
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            if (i > 0) __syncthreads();  // the first eight are read
+            if ((lane >> 2) < live) {
+                float* row = buf + (8 * warp + (lane >> 2)) * G::kPad + 2 * (lane & 3);
 #pragma unroll
-                        for (int d = 0; d < DIM / 8; ++d)
-                            finish(r, 8 * d + 2 * (lane & 3), m[i], l[i], o[d][2 * i], o[d][2 * i + 1]);
+                for (int d = 0; d < DIM / 8; ++d) *reinterpret_cast<float2*>(row + 8 * d) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
+                if ((lane & 3) == 0) *reinterpret_cast<float2*>(buf_ml + 2 * (8 * warp + (lane >> 2))) = make_float2(m[i], l[i]);
+            }
+            __syncthreads();
+            for (int x = threadIdx.x; x < live * (DIM / 4); x += kSplitThreads) {
+                const int r = x / (DIM / 4), d = x % (DIM / 4) * 4;
+                float2 ml[kSplitWarps];
+                float M = -INFINITY, L = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kSplitWarps; ++w) {
+                    ml[w] = *reinterpret_cast<const float2*>(buf_ml + 2 * (8 * w + r));
+                    M = fmaxf(M, ml[w].x);
+                }
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kSplitWarps; ++w) {
+                    const float a = ml[w].x == -INFINITY ? 0.0f : exp2_approx(ml[w].x - M);
+                    const float4 v = *reinterpret_cast<const float4*>(buf + (8 * w + r) * G::kPad + d);
+                    L += a * ml[w].y;
+                    acc.x += a * v.x, acc.y += a * v.y, acc.z += a * v.z, acc.w += a * v.w;
+                }
+                if (wf == wl) {
+                    finish(8 * i + r, d, M, L, acc);
+                } else {
+                    float* to = (blockIdx.x == wf ? wf_slot : slot_of(blockIdx.x)) + (8 * i + r) * DIM;
+                    *reinterpret_cast<float4*>(to + d) = acc;
+                    if (d == 0) *reinterpret_cast<float2*>(to - (8 * i + r) * DIM + kRows * DIM + 2 * (8 * i + r)) = make_float2(M, L);
                 }
             }
-        } else {
-            const auto slot_of = [&](int64_t w) { return partials + (2 * w + (w == wf && wf * U / N < cur.begin ? 1 : 0)) * partial_floats<DIM>(); };
-            if (warp == 0) {
-                float* to = slot_of(blockIdx.x);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = (lane >> 2) + 8 * i;
-                    if (r < rows) {
-#pragma unroll
-                        for (int d = 0; d < DIM / 8; ++d)
-                            *reinterpret_cast<float2*>(to + r * DIM + 8 * d + 2 * (lane & 3)) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
-                        if ((lane & 3) == 0) to[kRows * DIM + r] = m[i], to[kRows * DIM + kRows + r] = l[i];
-                    }
-                }
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) {
-                    const unsigned n = atomicAdd(&counters[wf], 1u);
-                    last_flag = n == unsigned(wl - wf);
-                    if (last_flag) counters[wf] = 0;  // for the next call
-                }
+        }
+        if (wf != wl) {
+            // ---- this worker's part is written; the last to arrive joins all
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const unsigned n = atomicAdd(&counters[wf], 1u);
+                last_flag = n == unsigned(wl - wf);
+                if (last_flag) counters[wf] = 0;  // for the next call
             }
             __syncthreads();
             if (last_flag) {
                 __threadfence();
-                const int live = rows < kRows ? rows : kRows;
-                for (int i = threadIdx.x; i < live * (DIM / 4); i += kSplitThreads) {
-                    const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
-                    float M = -INFINITY, L = 0.0f;
-                    for (int64_t w = wf; w <= wl; ++w) M = fmaxf(M, __ldcg(slot_of(w) + kRows * DIM + r));
-                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int64_t w = wf; w <= wl; ++w) {
-                        const float* f = slot_of(w);
-                        const float wm = __ldcg(f + kRows * DIM + r), wlen = __ldcg(f + kRows * DIM + kRows + r);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(f + r * DIM + d));
-                        const float a = wm == -INFINITY ? 0.0f : exp2_approx(wm - M);
-                        L += a * wlen;
-                        acc.x += a * v.x, acc.y += a * v.y, acc.z += a * v.z, acc.w += a * v.w;
+                const int live = rows < kRows ? rows : kRows, parts = int(wl - wf);  // beyond the first
+                const float* rest = slot_of(wf + 1);
+                constexpr int64_t kStep = 2 * partial_floats<DIM>();
+                for (int x = threadIdx.x; x < live * (DIM / 4); x += kSplitThreads) {
+                    const int r = x / (DIM / 4), d = x % (DIM / 4) * 4;
+                    const int at_ml = kRows * DIM + 2 * r, at_o = r * DIM + d;
+                    float2 ml = __ldcg(reinterpret_cast<const float2*>(wf_slot + at_ml));
+                    float M = ml.x, L = ml.y;
+                    float4 acc = __ldcg(reinterpret_cast<const float4*>(wf_slot + at_o));
+                    // eight parts' loads in flight at a time
+                    for (int w0 = 0; w0 < parts; w0 += 8) {
+                        float2 e[8];
+                        float4 v[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const float* f = rest + (w0 + y < parts ? w0 + y : parts - 1) * kStep;
+                            e[y] = __ldcg(reinterpret_cast<const float2*>(f + at_ml));
+                            v[y] = __ldcg(reinterpret_cast<const float4*>(f + at_o));
+                        }
+                        float mn = M;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) mn = fmaxf(mn, e[y].x);
+                        const float a = M == -INFINITY ? 0.0f : exp2_approx(M - mn);
+                        M = mn;
+                        L *= a, acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const float c = w0 + y < parts && e[y].x != -INFINITY ? exp2_approx(e[y].x - mn) : 0.0f;
+                            L += c * e[y].y;
+                            acc.x += c * v[y].x, acc.y += c * v[y].y, acc.z += c * v[y].z, acc.w += c * v[y].w;
+                        }
                     }
-                    finish(r, d, M, L, acc.x, acc.y);
-                    finish(r, d + 2, M, L, acc.z, acc.w);
+                    finish(r, d, M, L, acc);
                 }
             }
+        } else {
+            __syncthreads();  // the buffer is read
         }
-        if (u + 1 < last) next_tile(p, cur, group);
     }
     cp_async_wait<0>();
+    if (p.beside) pdl_wait_prior_grid();  // complete only after that kernel, too
 }
 
 template <typename T, int DIM>
@@ -612,11 +637,13 @@ cudaError_t launch_split(const SplitParams& p, int sm_count, cudaStream_t s) {
     return launch_serial(attn_split_kernel<T, DIM>, dim3(unsigned(workers)), kSplitThreads, SplitGeom<DIM>::kSmem, s, p);
 }
 
-cudaError_t launch_split_any(int dtype, const AttnParams& a, float* part_o, float* part_lse, int sm_count, cudaStream_t s) {
+cudaError_t launch_split_any(int dtype, const AttnParams& a, float* part_o, float* part_lse, bool beside, int sm_count,
+                             cudaStream_t s) {
     SplitParams p;
     static_cast<AttnParams&>(p) = a;
     p.part_o = part_o;
     p.part_lse = part_lse;
+    p.beside = beside ? 1 : 0;
     const bool f16 = dtype == QX_F16;
     if (a.kv.head_dim == 128)
         return f16 ? launch_split<__half, 128>(p, sm_count, s) : launch_split<__nv_bfloat16, 128>(p, sm_count, s);
@@ -685,10 +712,10 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
         float* o = part_o + j.parts * rows * dim;
         float* l = part_lse + j.parts * rows;
         ++j.parts;
-        e = many ? launch_attn_tc(dtype, p, false, 1, o, l, counter, sm_count, s) : launch_split_any(dtype, p, o, l, sm_count, s);
+        e = many ? launch_attn_tc(dtype, p, false, 1, o, l, counter, sm_count, s) : launch_split_any(dtype, p, o, l, true, sm_count, s);
         return e != cudaSuccess ? e : launch_attn_join(dtype, j, s);
     }
-    if (!many) return launch_split_any(dtype, p, nullptr, nullptr, sm_count, s);
+    if (!many) return launch_split_any(dtype, p, nullptr, nullptr, false, sm_count, s);
     const int n = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, false) * p.kv.n_heads, rows, spare, sm_count);
     if (n == 1) return launch_attn_tc(dtype, p, false, 1, nullptr, nullptr, counter, sm_count, s);
     if ((e = launch_attn_tc(dtype, p, false, n, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
