@@ -118,28 +118,31 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_row_kernel(const __grid_c
 // the others' (m, l, o) in the order of the workers, so the result does not
 // depend on who is last.
 //
-// In a CTA each of four warps takes 16 of a unit's keys with an online
-// softmax of its own: it copies its keys and values to its own ring in shared
-// memory (cp.async, whole 16-byte chunks, chunk c of row r at c ^ (r % 8) so
-// that ldmatrix meets no bank conflict) and needs no other warp until the
-// tile ends.  Products: mma.sync m16n8k16, whose 16 rows the group fills at
-// most partly; the tensor pipe is not what bounds this kernel.
+// In a CTA a producer warp walks the line and fetches the units by TMA (one
+// box a page, 128-byte swizzle, so that ldmatrix meets no bank conflict) into
+// a ring of 96 KB, 64 KB of it ahead of the products; each of four warps takes
+// 16 of a unit's keys with an online softmax of its own and meets the others
+// only where the tile ends.  Products: mma.sync m16n8k16, whose 16 rows the
+// group fills at most partly; the tensor pipe is not what bounds this kernel.
 
 constexpr int kUnit = 64;                // keys of a unit
+constexpr uint64_t kSplitWaitNs = 2000000000ull;
 constexpr int kSplitWarps = 4;
-constexpr int kSplitThreads = 32 * kSplitWarps;
+constexpr int kSplitThreads = 32 * (kSplitWarps + 1);  // the last warp is the producer
 constexpr int kRows = 16;                // rows of a tile
 constexpr int kRingBytes = 96 * 1024;    // of one CTA; two CTAs fit on an SM
 
 template <int DIM>
 struct SplitGeom {
-    static constexpr int kRowBytes = 2 * DIM;
-    static constexpr int kStageBytes = 2 * 16 * kRowBytes;  // one warp's keys and values
-    static constexpr int kStages = kRingBytes / (kSplitWarps * kStageBytes);
+    static constexpr int kPanels = DIM / 64;                  // 64 elements (128 bytes) of every key
+    static constexpr int kPanelBytes = kUnit * 128;
+    static constexpr int kHalfStage = kPanels * kPanelBytes;  // a unit's keys; its values follow
+    static constexpr int kStages = kRingBytes / (2 * kHalfStage);
     static constexpr int kPad = DIM + 4;  // floats of a row in the joining buffer: 8 rows of each warp, then their m and l
     static constexpr int kJoin = (kSplitWarps * 8 * (kPad + 2)) * 4;
-    static constexpr size_t kSmem = kRingBytes + kJoin;
-    static_assert(2 * (kSmem + 1200) <= 228 * 1024, "two CTAs an SM");
+    static constexpr int kMisc = 256;     // barriers, the worker's place on the line
+    static constexpr size_t kSmem = kRingBytes + kJoin + kMisc;
+    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
 // Scratch: arrival counters (one a worker, and 64 words for the tensor-core
@@ -149,14 +152,6 @@ constexpr size_t kCounterBytes = (kMaxWorkers + 64) * 4;
 template <int DIM>
 __host__ __device__ constexpr int partial_floats() { return kRows * DIM + 2 * kRows; }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldmatrix4(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -191,40 +186,39 @@ struct SeqWork {
     int t0, tokens;        // first token, tokens
     int row_tiles;         // tiles of 16 rows for each key head
     int sink_units, units; // of one tile
-    int64_t pos0;          // position of the first token
-    int64_t lo, end, sinks;
+    int pos0;              // position of the first token
+    int lo, end, sinks;
 };
+constexpr int kMostKeys = INT32_MAX - 4 * kUnit;  // of a sequence: key numbers stay in 32 bits
 __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, int group, bool report) {
     SeqWork w;
     w.t0 = p.kv.q_start[b];
     w.tokens = p.kv.q_start[b + 1] - w.t0;
+    const int kv = p.kv.kv_len[b];
     if (w.tokens < 0 || w.t0 < 0 || w.t0 + w.tokens > p.n_tokens) w.tokens = 0;  // not an ascending list of this call's tokens
-    int64_t kv = p.kv.kv_len[b];
     w.pos0 = kv - w.tokens;
-    const int64_t most = p.kv.table_stride << p.kv.page_shift;
-    if (kv > most) {
-        if (report) atomicOr(p.kv.err, kErrRange);
-        kv = most;
-    }
-    w.end = kv < 0 ? 0 : kv;
-    w.lo = p.window > 0 && w.pos0 + 1 > p.window ? w.pos0 + 1 - p.window : 0;
-    if (w.lo < p.shared_len) w.lo = p.shared_len;
-    w.sinks = p.sinks < w.lo ? p.sinks : w.lo;
-    if (p.shared_len > 0) w.sinks = 0;
-    if (w.sinks > w.end) w.sinks = w.end;
-    w.sink_units = int((w.sinks + kUnit - 1) / kUnit);
-    const int64_t win = (w.end + kUnit - 1) / kUnit - w.lo / kUnit;
-    w.units = w.sink_units + (win > 0 ? int(win) : 0);
+    const int64_t room = p.kv.table_stride << p.kv.page_shift;
+    const int most = room < kMostKeys ? int(room) : kMostKeys;
+    if (kv > most && report) atomicOr(p.kv.err, kErrRange);
+    w.end = kv < 0 ? 0 : kv < most ? kv : most;
+    const int window = p.window < INT32_MAX ? int(p.window) : 0;
+    const int shared = p.shared_len < INT32_MAX ? int(p.shared_len) : INT32_MAX;
+    w.lo = window > 0 && w.pos0 >= window ? w.pos0 - window + 1 : 0;
+    if (w.lo < shared) w.lo = shared;
+    if (w.lo > w.end) w.lo = w.end;
+    w.sinks = shared > 0 ? 0 : p.sinks < w.lo ? int(p.sinks) : w.lo;
+    w.sink_units = (w.sinks + kUnit - 1) / kUnit;
+    w.units = w.sink_units + (w.end > w.lo ? (w.end + kUnit - 1) / kUnit - w.lo / kUnit : 0);
     if (w.units < 1) w.units = 1;
     w.row_tiles = (w.tokens * group + kRows - 1) / kRows;
     return w;
 }
 
-// A place on the line of units: unit u of tile (sequence b, row tile rt, key
-// head hk), where the tile's units are [begin, begin + w.units) of the line.
+// A place on the line of units: tile (sequence b, row tile rt, key head hk),
+// whose units are [begin, begin + w.units) of the line.
 struct Cursor {
-    int b, rt, hk;
     int64_t begin;
+    int b, rt, hk;
     SeqWork w;
 };
 __device__ __forceinline__ void next_tile(const AttnParams& p, Cursor& c, int group) {
@@ -239,16 +233,17 @@ __device__ __forceinline__ void next_tile(const AttnParams& p, Cursor& c, int gr
     } while (c.w.row_tiles == 0);
 }
 // The first key of unit u of a tile, and the keys [lo, hi) of it that any row sees.
-__device__ __forceinline__ int64_t unit_keys(const SeqWork& w, int u, int64_t& lo, int64_t& hi) {
-    if (u < w.sink_units) {
-        lo = 0, hi = w.sinks;
-        return int64_t(u) * kUnit;
-    }
-    lo = w.lo, hi = w.end;
-    return (w.lo / kUnit + (u - w.sink_units)) * kUnit;
+__device__ __forceinline__ int unit_keys(const SeqWork& w, int u, int& lo, int& hi) {
+    const bool sink = u < w.sink_units;
+    lo = sink ? 0 : w.lo;
+    hi = sink ? w.sinks : w.end;
+    return (sink ? u : w.lo / kUnit + (u - w.sink_units)) * kUnit;
 }
 
-struct SplitParams : AttnParams {
+struct SplitParams {
+    CUtensorMap k_map;  // [pages][heads][slots][dim], boxes of min(page, 64) keys x 64
+    CUtensorMap v_map;
+    AttnParams a;
     float* part_o;    // not null: the rows are a part to be joined (o / l, base-2 log of the sum)
     float* part_lse;
     int beside;       // 1: launched beside the kernel before it, which belongs to the same call
@@ -259,27 +254,45 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
     if (((a | b) >> 32) == 0) return int64_t(uint32_t(a) / uint32_t(b));
     return a / b;
 }
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSplitWarps) : "memory"); }
 
 template <typename T, int DIM>
-__global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __grid_constant__ SplitParams p) {
+__global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __grid_constant__ SplitParams pp) {
     using G = SplitGeom<DIM>;
     constexpr int KS = DIM / 16;  // 16-wide steps along a head
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t scan[kSplitWarps];
-    __shared__ Cursor start;
-    __shared__ int last_flag;
+    constexpr int NS = G::kStages;
+    const AttnParams& p = pp.a;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float* buf = reinterpret_cast<float*>(smem + kRingBytes);  // [4 warps][8 rows][kPad], then m and l of each
+    float* buf_ml = buf + kSplitWarps * 8 * G::kPad;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes + G::kJoin);
+    uint64_t* empty = full + NS;
+    int64_t* scan = reinterpret_cast<int64_t*>(empty + NS);  // [5]
+    Cursor* start = reinterpret_cast<Cursor*>(scan + kSplitWarps + 1);
+    int* last_flag = reinterpret_cast<int*>(start + 1);
+    static_assert((2 * NS + kSplitWarps + 1) * 8 + sizeof(Cursor) + 4 <= G::kMisc, "barriers and the worker's place");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kSplitWarps);
+        }
+        fence_barrier_init();
+        prefetch_map(&pp.k_map);
+        prefetch_map(&pp.v_map);
+    }
     // Beside a kernel that works on the same call's prefix: that one has
     // waited for the work before it, and this one reads nothing of its.
-    if (!p.beside) pdl_wait_prior_grid();
+    if (!pp.beside) pdl_wait_prior_grid();
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = p.n_q_heads / p.kv.n_heads;
     const int B = p.kv.n_seqs;
 
     // ---- the line's length, and where this worker's share begins
     int64_t mine = 0;
     const int per = (B + kSplitThreads - 1) / kSplitThreads, b0 = threadIdx.x * per;
-    SeqWork own;  // of the thread's last sequence (its only one, for up to 128 sequences)
+    SeqWork own;  // of the thread's last sequence (its only one, for up to 160 sequences)
     for (int b = b0; b < b0 + per && b < B; ++b) {
         own = seq_work(p, b, group, blockIdx.x == 0);
         mine += int64_t(own.row_tiles) * p.kv.n_heads * own.units;
@@ -294,13 +307,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     __syncthreads();
     int64_t U = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < kSplitWarps; ++w) {
+    for (int w = 0; w <= kSplitWarps; ++w) {
         if (w < warp) before += scan[w];
         U += scan[w];
     }
     const int64_t N = gridDim.x < U ? gridDim.x : U;
     if (blockIdx.x >= N) {
-        if (p.beside) pdl_wait_prior_grid();
+        if (pp.beside) pdl_wait_prior_grid();
         return;
     }
     // the first `extra` workers have one unit more than the others
@@ -317,74 +330,98 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
             const int64_t n = int64_t(own.row_tiles) * p.kv.n_heads * own.units;
             if (first < at + n) {
                 const int64_t tile = quot(first - at, own.units);
-                start.b = b;
-                start.w = own;
-                start.begin = at + tile * own.units;
-                start.rt = int(quot(tile, p.kv.n_heads));
-                start.hk = int(tile - int64_t(start.rt) * p.kv.n_heads);
+                start->b = b;
+                start->w = own;
+                start->begin = at + tile * own.units;
+                start->rt = int(quot(tile, p.kv.n_heads));
+                start->hk = int(tile - int64_t(start->rt) * p.kv.n_heads);
                 break;
             }
             at += n;
         }
     }
     __syncthreads();
-    Cursor ld = start;   // of the unit being fetched
-    Cursor cur = start;  // of the unit being computed
+    Cursor cur = *start;
+    int ui = int(first - cur.begin);  // unit of the tile
+    int64_t left = last - first;      // units to go
 
-    // ---- this warp's ring
-    uint8_t* ring = smem + warp * (G::kStages * G::kStageBytes);
-    const uint32_t ring_a = smem_addr(ring);
-    int64_t fu = first;  // the next unit to fetch
-    // Sixteen keys of unit u from key 16 * warp of it on: their page, or -1
-    // where no row sees any of them.
-    const auto page_for = [&](const Cursor& c, int64_t u) -> int {
-        int64_t lo, hi;
-        const int64_t j0 = unit_keys(c.w, int(u - c.begin), lo, hi) + 16 * warp;
-        if (j0 + 16 <= lo || j0 >= hi) return -1;
-        return page_of(p.kv, c.b, j0);
-    };
-    int page = page_for(ld, fu);
-    const auto fetch = [&](int stage) {
-        if (fu < last) {
-            int64_t lo, hi;
-            const int64_t j0 = unit_keys(ld.w, int(fu - ld.begin), lo, hi) + 16 * warp;
-            const int64_t base = page < 0 ? 0 : slot_offset(p.kv, page, ld.hk, j0);
-            const T* ks = reinterpret_cast<const T*>(p.kv.k) + base;
-            const T* vs = reinterpret_cast<const T*>(p.kv.v) + base;
-            constexpr int CH = G::kRowBytes / 16;  // chunks of a row
-            const uint32_t dst = ring_a + stage * G::kStageBytes;
-#pragma unroll
-            for (int i = 0; i < 16 * CH / 32; ++i) {
-                const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
-                const bool live = page >= 0 && j0 + r >= lo && j0 + r < hi;
-                const int64_t off = live ? r * p.kv.slot_stride + c * 8 : 0;
-                const uint32_t d = dst + r * G::kRowBytes + ((c ^ (r & 7)) << 4);
-                cp_async16(d, ks + off, live);
-                cp_async16(d + 16 * G::kRowBytes, vs + off, live);
+    if (warp == kSplitWarps) {
+        // ---- producer: a lane for each page of a unit
+        const int page_keys = (1 << p.kv.page_shift) < kUnit ? (1 << p.kv.page_shift) : kUnit;
+        const int in_page_mask = (1 << p.kv.page_shift) - 1;
+        const int boxes = kUnit / page_keys;  // at most 4
+        // the lane's page of unit ui, or -1 where no row sees any of its keys
+        const auto page_for = [&](int u) -> int {
+            int lo, hi;
+            const int j = unit_keys(cur.w, u, lo, hi) + lane * page_keys;
+            return lane < boxes && j + page_keys > lo && j < hi ? page_of(p.kv, cur.b, j) : -1;
+        };
+        int page = page_for(ui);
+        int slot = 0;
+        uint32_t phase = 1;  // the ring is empty at first: the wait for the phase before the first returns
+        bool ok = true;
+        int used = 0;
+        for (; left > 0; --left) {
+            int lo, hi;
+            const int j0 = unit_keys(cur.w, ui, lo, hi);
+            const int in_page = (j0 + lane * page_keys) & in_page_mask, hk = cur.hk, now = page;
+            if (left > 1) {  // the next unit's pages are looked up while this one's room is awaited
+                if (++ui == cur.w.units) {
+                    next_tile(p, cur, group);
+                    ui = 0;
+                }
+                page = page_for(ui);
             }
-            if (++fu < last) {
-                if (fu == ld.begin + ld.w.units) next_tile(p, ld, group);
-                page = page_for(ld, fu);
+            const unsigned live = __ballot_sync(0xffffffffu, now >= 0);
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[slot], phase, kSplitWaitNs, p.kv.err, kErrTimeoutEmpty));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(live) * page_keys * 128 * G::kPanels * 2);
+            __syncwarp();
+            if (now >= 0) {
+                uint8_t* dst = smem + slot * 2 * G::kHalfStage + lane * page_keys * 128;
+#pragma unroll
+                for (int c = 0; c < G::kPanels; ++c) {
+                    tma_load_4d(dst + c * G::kPanelBytes, &pp.k_map, 64 * c, in_page, hk, now, &full[slot]);
+                    tma_load_4d(dst + G::kHalfStage + c * G::kPanelBytes, &pp.v_map, 64 * c, in_page, hk, now, &full[slot]);
+                }
+            }
+            if (used < NS) ++used;
+            if (++slot == NS) {
+                slot = 0;
+                phase ^= 1;
             }
         }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < G::kStages - 1; ++s) fetch(s);
+        // keep the CTA alive until every copy it issued has landed
+        if (lane == 0) {
+            for (int i = 0; i < used; ++i) {  // the last `used` slots, most recent first
+                if (--slot < 0) {
+                    slot = NS - 1;
+                    phase ^= 1;
+                }
+                mbar_wait_bounded(&full[slot], phase ^ 1, kSplitWaitNs, p.kv.err, kErrTimeoutDrain);
+            }
+        }
+        if (pp.beside) pdl_wait_prior_grid();
+        return;
+    }
 
-    // ---- units
+    // ---- consumers
     uint32_t qf[KS][4];
     float o[DIM / 8][4], m[2], l[2];
-    int64_t rpos[2];  // positions of this lane's two rows (-1: none)
+    int rpos[2];             // positions of this lane's two rows (-1: none)
+    int pos_first, pos_last; // of the tile's rows
     // A tile's rows: 16 rt + lane / 4 and eight further.
     const auto open_tile = [&](const Cursor& c) {
-        const int rows = c.w.tokens * group;
+        const int rows = c.w.tokens * group, r0 = kRows * c.rt;
+        pos_first = c.w.pos0 + r0 / group;
+        pos_last = c.w.pos0 + (r0 + kRows < rows ? r0 + kRows - 1 : rows - 1) / group;
+        if (pos_last < -1) pos_last = -1;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int r = kRows * c.rt + (lane >> 2) + 8 * i;
+            const int r = r0 + (lane >> 2) + 8 * i;
             const bool live = r < rows;
             const int tok = live ? r / group : 0, g = live ? r - tok * group : 0;
-            rpos[i] = live ? c.w.pos0 + tok : -1;
+            rpos[i] = live && c.w.pos0 + tok >= 0 ? c.w.pos0 + tok : -1;
             const T* q = static_cast<const T*>(p.q) + int64_t(c.w.t0 + tok) * p.q_stride + int64_t(c.hk * group + g) * DIM + 2 * (lane & 3);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
@@ -396,58 +433,80 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     open_tile(cur);
     float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(p.scratch) + kCounterBytes);
     unsigned* counters = static_cast<unsigned*>(p.scratch);
-    float* buf = reinterpret_cast<float*>(smem + kRingBytes);  // [4 warps][8 rows][kPad], then m and l of each
-    float* buf_ml = buf + kSplitWarps * 8 * G::kPad;
-    int stage = 0;
-    for (int64_t u = first; u < last; ++u) {
-        if (u == first || u == cur.begin) {
+    const int window = p.window > 0 && p.window < INT32_MAX ? int(p.window) : INT32_MAX;
+    const int sinks = p.sinks < INT32_MAX ? int(p.sinks) : INT32_MAX;
+    // This lane's part of the ldmatrix addresses, relative to a stage: keys
+    // 16 warp + (0-7 and 8-15 by d 0-7 and 8-15 of a step), and values 16 warp
+    // + (0-15 by d 0-7 and 8-15).
+    const uint32_t ring = smem_addr(smem);
+    const int kr = 16 * warp + (lane & 7) + ((lane >> 4) << 3), kh = (lane >> 3) & 1;
+    const int vr = 16 * warp + (lane & 15), vh = lane >> 4;
+    const uint32_t k_row = ring + kr * 128, v_row = ring + G::kHalfStage + vr * 128;
+    int slot = 0;
+    uint32_t phase = 0;
+    bool fresh = true, ok = true;
+    for (; left > 0; --left) {
+        if (fresh) {
             m[0] = m[1] = -INFINITY;
             l[0] = l[1] = 0.0f;
 #pragma unroll
             for (int d = 0; d < DIM / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.0f;
+            fresh = false;
         }
-        cp_async_wait<G::kStages - 2>();
-        __syncwarp();
-        int64_t lo, hi;
-        const int64_t j0 = unit_keys(cur.w, int(u - cur.begin), lo, hi) + 16 * warp;
+        int lo, hi;
+        const int j0 = unit_keys(cur.w, ui, lo, hi) + 16 * warp;  // this warp's sixteen keys
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], phase, kSplitWaitNs, p.kv.err, kErrTimeoutFull));
+        if (!ok) break;
         if (j0 + 16 > lo && j0 < hi) {
-            const uint32_t ka = ring_a + stage * G::kStageBytes, va = ka + 16 * G::kRowBytes;
+            const uint32_t off = slot * 2 * G::kHalfStage;
             float s[2][4] = {};
-            {
-                // matrices: keys 0-7 and 8-15 by d 0-7 and 8-15 of each step
-                const int r = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t b[4];
-                    ldmatrix4(ka + r * G::kRowBytes + (((2 * k + half) ^ (r & 7)) << 4), b);
-                    mma16816<T>(s[0], qf[k], b[0], b[1]);
-                    mma16816<T>(s[1], qf[k], b[2], b[3]);
+            for (int k = 0; k < KS; ++k) {
+                uint32_t b[4];
+                ldmatrix4(k_row + off + (k >> 2) * G::kPanelBytes + (((2 * (k & 3) + kh) ^ (kr & 7)) << 4), b);
+                mma16816<T>(s[0], qf[k], b[0], b[1]);
+                mma16816<T>(s[1], qf[k], b[2], b[3]);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] *= p.scale_log2;
+            const bool sink_unit = ui < cur.w.sink_units;
+            if (j0 < lo || j0 + 16 > hi || j0 + 15 > pos_first || (!sink_unit && pos_last - window >= j0)) {
+                // some row does not see some of them.  This lane's keys,
+                // relative to the first: 2 (lane % 4) + {0, 1, 8, 9}.
+                const int a = lo - j0, b = hi - j0, c = sinks - j0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int end = rpos[i] - j0 + 1 < b ? rpos[i] - j0 + 1 : b;
+                    const int low = rpos[i] >= window ? rpos[i] - window + 1 : 0;  // of the row's window
+                    const int from = sink_unit || low - j0 < a ? a : low - j0;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = 8 * n + 2 * (lane & 3) + e;
+                            if (!(j < end && (j >= from || (j >= a && j < c)))) s[n][2 * i + e] = -INFINITY;
+                        }
+                }
+                // Values that no row sees are zeroed: whatever the slots hold, 0 x it must be 0.
+                if (j0 < lo || j0 + 16 > hi) {
+                    if (vr - 16 * warp < a || vr - 16 * warp >= b) {
+#pragma unroll
+                        for (int c2 = 0; c2 < G::kPanels; ++c2)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                *reinterpret_cast<uint4*>(smem + slot * 2 * G::kHalfStage + G::kHalfStage + c2 * G::kPanelBytes + vr * 128 +
+                                                          64 * vh + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();  // before the slot's next copy
+                    __syncwarp();
                 }
             }
-            // This lane's keys relative to the sixteen's first: 2 (lane % 4) + {0, 1, 8, 9}.
-            const bool sink_unit = u - cur.begin < cur.w.sink_units;
-            const int first_key = lo > j0 ? int(lo - j0) : 0, end_key = hi < j0 + 16 ? int(hi - j0) : 16;
-            float mx[2] = {m[0], m[1]};
+            float mx[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t back = rpos[i] - j0;  // the row's position among them
-                const int end = back < end_key - 1 ? int(back < -1 ? -1 : back) + 1 : end_key;
-                int from = first_key, sink_end = 0;
-                if (p.window > 0 && !sink_unit) {
-                    const int64_t f = back - p.window + 1;
-                    from = f > first_key ? (f < 16 ? int(f) : 16) : first_key;
-                    const int64_t e = p.sinks - j0;
-                    sink_end = e < 0 ? 0 : e < 16 ? int(e) : 16;
-                }
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = 8 * n + 2 * (lane & 3) + e;
-                        const bool see = j < end && (j >= from || (j >= first_key && j < sink_end));
-                        s[n][2 * i + e] = see ? s[n][2 * i + e] * p.scale_log2 : -INFINITY;
-                        mx[i] = fmaxf(mx[i], s[n][2 * i + e]);
-                    }
+                mx[i] = fmaxf(m[i], fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1])));
                 mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
                 mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
             }
@@ -476,50 +535,47 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                 }
             const uint32_t pf[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]), pack2<T>(s[1][0], s[1][1]),
                                     pack2<T>(s[1][2], s[1][3])};
-            {
-                const int r = lane & 15, half = lane >> 4;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t b[4];
-                    ldmatrix4_t(va + r * G::kRowBytes + (((2 * k + half) ^ (r & 7)) << 4), b);
-                    mma16816<T>(o[2 * k], pf, b[0], b[1]);
-                    mma16816<T>(o[2 * k + 1], pf, b[2], b[3]);
-                }
+            for (int k = 0; k < KS; ++k) {
+                uint32_t b[4];
+                ldmatrix4_t(v_row + off + (k >> 2) * G::kPanelBytes + (((2 * (k & 3) + vh) ^ (vr & 7)) << 4), b);
+                mma16816<T>(o[2 * k], pf, b[0], b[1]);
+                mma16816<T>(o[2 * k + 1], pf, b[2], b[3]);
             }
         }
-        __syncwarp();  // the stage is free again
-        {
-            int fs = stage + G::kStages - 1;
-            if (fs >= G::kStages) fs -= G::kStages;
-            fetch(fs);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        if (++slot == NS) {
+            slot = 0;
+            phase ^= 1;
         }
-        if (++stage == G::kStages) stage = 0;
-
-        const int64_t t_end = cur.begin + cur.w.units;
-        if (u + 1 != last && u + 1 != t_end) continue;
+        if (++ui < cur.w.units && left > 1) continue;
         // ---- the tile ends here (for this worker).  The next one's queries
         // are on their way while its warps are joined, eight rows at a time:
         // every warp leaves its (m, l, o), and every thread then joins some
         // elements.
-        const Cursor done = cur;
-        if (u + 1 < last) {
+        const int rt = cur.rt, hk = cur.hk, t0 = cur.w.t0;
+        const int rows = cur.w.tokens * group - kRows * rt;  // of this tile (16 at most count)
+        const int64_t t_begin = cur.begin, t_end = cur.begin + cur.w.units;
+        if (left > 1) {
             next_tile(p, cur, group);
             open_tile(cur);
+            ui = 0;
+            fresh = true;
         }
-        const int rows = done.w.tokens * group - kRows * done.rt;  // of this tile (16 at most count)
-        const int64_t wf = worker_of(done.begin), wl = worker_of(t_end - 1);  // the first and last worker of the tile
+        const int64_t wf = worker_of(t_begin), wl = worker_of(t_end - 1);  // the first and last worker of the tile
         // A worker's part of a tile lies in its first slot, or in its second
         // where another tile's end came first.
         const auto slot_of = [&](int64_t w) -> float* { return partials + 2 * w * partial_floats<DIM>(); };
-        float* const wf_slot = slot_of(wf) + (begin_of(wf) < done.begin ? partial_floats<DIM>() : 0);
+        float* const wf_slot = slot_of(wf) + (begin_of(wf) < t_begin ? partial_floats<DIM>() : 0);
         const auto finish = [&](int r, int d, float M, float L, float4 v) {
-            const int rr = kRows * done.rt + r;
-            const int64_t row = int64_t(done.w.t0 + rr / group) * p.n_q_heads + done.hk * group + rr % group;
+            const int rr = kRows * rt + r;
+            const int64_t row = int64_t(t0 + rr / group) * p.n_q_heads + hk * group + rr % group;
             const float inv = L > 0.0f ? 1.0f / L : 0.0f;
             v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-            if (p.part_o) {
-                *reinterpret_cast<float4*>(p.part_o + row * DIM + d) = v;
-                if (d == 0) p.part_lse[row] = L > 0.0f ? M + log2f(L) : -INFINITY;
+            if (pp.part_o) {
+                *reinterpret_cast<float4*>(pp.part_o + row * DIM + d) = v;
+                if (d == 0) pp.part_lse[row] = L > 0.0f ? M + log2f(L) : -INFINITY;
                 return;
             }
             if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * DIM + d) = v;
@@ -532,15 +588,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
             const int live = rows - 8 * i < 8 ? rows - 8 * i : 8;
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            if (i > 0) __syncthreads();  // the first eight are read
+            if (i > 0) consumers_sync();  // the first eight are read
             if ((lane >> 2) < live) {
                 float* row = buf + (8 * warp + (lane >> 2)) * G::kPad + 2 * (lane & 3);
 #pragma unroll
                 for (int d = 0; d < DIM / 8; ++d) *reinterpret_cast<float2*>(row + 8 * d) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
                 if ((lane & 3) == 0) *reinterpret_cast<float2*>(buf_ml + 2 * (8 * warp + (lane >> 2))) = make_float2(m[i], l[i]);
             }
-            __syncthreads();
-            for (int x = threadIdx.x; x < live * (DIM / 4); x += kSplitThreads) {
+            consumers_sync();
+            for (int x = threadIdx.x; x < live * (DIM / 4); x += 32 * kSplitWarps) {
                 const int r = x / (DIM / 4), d = x % (DIM / 4) * 4;
                 float2 ml[kSplitWarps];
                 float M = -INFINITY, L = 0.0f;
@@ -560,31 +616,31 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                 if (wf == wl) {
                     finish(8 * i + r, d, M, L, acc);
                 } else {
-                    float* to = (blockIdx.x == wf ? wf_slot : slot_of(blockIdx.x)) + (8 * i + r) * DIM;
-                    *reinterpret_cast<float4*>(to + d) = acc;
-                    if (d == 0) *reinterpret_cast<float2*>(to - (8 * i + r) * DIM + kRows * DIM + 2 * (8 * i + r)) = make_float2(M, L);
+                    float* to = (blockIdx.x == wf ? wf_slot : slot_of(blockIdx.x));
+                    *reinterpret_cast<float4*>(to + (8 * i + r) * DIM + d) = acc;
+                    if (d == 0) *reinterpret_cast<float2*>(to + kRows * DIM + 2 * (8 * i + r)) = make_float2(M, L);
                 }
             }
         }
         if (wf != wl) {
             // ---- this worker's part is written; the last to arrive joins all
             __threadfence();
-            __syncthreads();
+            consumers_sync();
             if (threadIdx.x == 0) {
                 const unsigned n = atomicAdd(&counters[wf], 1u);
-                last_flag = n == unsigned(wl - wf);
-                if (last_flag) counters[wf] = 0;  // for the next call
+                *last_flag = n == unsigned(wl - wf);
+                if (*last_flag) counters[wf] = 0;  // for the next call
             }
-            __syncthreads();
-            if (last_flag) {
+            consumers_sync();
+            if (*last_flag) {
                 __threadfence();
                 const int live = rows < kRows ? rows : kRows, parts = int(wl - wf);  // beyond the first
                 const float* rest = slot_of(wf + 1);
                 constexpr int64_t kStep = 2 * partial_floats<DIM>();
-                for (int x = threadIdx.x; x < live * (DIM / 4); x += kSplitThreads) {
+                for (int x = threadIdx.x; x < live * (DIM / 4); x += 32 * kSplitWarps) {
                     const int r = x / (DIM / 4), d = x % (DIM / 4) * 4;
                     const int at_ml = kRows * DIM + 2 * r, at_o = r * DIM + d;
-                    float2 ml = __ldcg(reinterpret_cast<const float2*>(wf_slot + at_ml));
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(wf_slot + at_ml));
                     float M = ml.x, L = ml.y;
                     float4 acc = __ldcg(reinterpret_cast<const float4*>(wf_slot + at_o));
                     // eight parts' loads in flight at a time
@@ -613,16 +669,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                     finish(r, d, M, L, acc);
                 }
             }
-        } else {
-            __syncthreads();  // the buffer is read
         }
+        consumers_sync();  // the buffer is read
     }
-    cp_async_wait<0>();
-    if (p.beside) pdl_wait_prior_grid();  // complete only after that kernel, too
+    if (pp.beside) pdl_wait_prior_grid();  // complete only after that kernel, too
 }
 
 template <typename T, int DIM>
-cudaError_t launch_split(const SplitParams& p, int sm_count, cudaStream_t s) {
+cudaError_t launch_split(SplitParams& p, int sm_count, cudaStream_t s) {
+    if (!encode_cache_maps(!IsBf16<T>::value, p.a.kv, kUnit, &p.k_map, &p.v_map)) return cudaErrorInvalidValue;
     static bool ready[64] = {false};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -640,7 +695,7 @@ cudaError_t launch_split(const SplitParams& p, int sm_count, cudaStream_t s) {
 cudaError_t launch_split_any(int dtype, const AttnParams& a, float* part_o, float* part_lse, bool beside, int sm_count,
                              cudaStream_t s) {
     SplitParams p;
-    static_cast<AttnParams&>(p) = a;
+    p.a = a;
     p.part_o = part_o;
     p.part_lse = part_lse;
     p.beside = beside ? 1 : 0;

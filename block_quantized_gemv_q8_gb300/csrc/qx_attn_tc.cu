@@ -98,20 +98,6 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, bool b_mn_major) {
            (uint32_t(kTileRows >> 4) << 24);
 }
 
-__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-            smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
-        : "memory");
-}
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
@@ -347,6 +333,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             mbar_init(&w_empty[i], kSoftmaxWarps + 2);
         }
         fence_barrier_init();
+        prefetch_map(&p.q_map);
+        prefetch_map(&p.k_map);
+        prefetch_map(&p.v_map);
     }
     if (warp == kSoftmaxWarps) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "r"(512)
@@ -401,7 +390,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     mbar_arrive_expect_tx(q_full, tiles * G::kPanels * p.tile_tokens * group * 128);
                     for (int t = 0; t < tiles; ++t)
                         for (int c = 0; c < G::kPanels; ++c)
-                            tma_3d(sq + t * G::kTileBytes + c * G::kPanelBytes, &p.q_map, 64 * c, w.hk * group,
+                            tma_load_3d(sq + t * G::kTileBytes + c * G::kPanelBytes, &p.q_map, 64 * c, w.hk * group,
                                    w.t0 + t * p.tile_tokens, q_full);
                 }
                 __syncwarp();
@@ -426,7 +415,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         if (page >= 0) {
                             uint8_t* dst = ring + at.slot * G::kTileBytes + lane * page_keys * 128;
                             for (int c = 0; c < G::kPanels; ++c)
-                                tma_4d(dst + c * G::kPanelBytes, v ? &p.v_map : &p.k_map, 64 * c, in_page, w.hk, page,
+                                tma_load_4d(dst + c * G::kPanelBytes, v ? &p.v_map : &p.k_map, 64 * c, in_page, w.hk, page,
                                        &kv_full[at.slot]);
                         }
                         ++issued;
@@ -827,15 +816,10 @@ cudaError_t launch_tc(const AttnParams& a, bool prefix, int splits, float* part_
     p.counter = counter;
     const int group = a.n_q_heads / a.kv.n_heads;
     p.tile_tokens = kTileRows / group;
-    const int page = 1 << a.kv.page_shift;
     const bool f16 = !IsBf16<T>::value;
-    const int64_t kd[4] = {DIM, page, a.kv.n_heads, a.kv.n_pages};
-    const int64_t ks[4] = {1, a.kv.slot_stride, a.kv.head_stride, a.kv.page_stride};
-    const int kb[4] = {64, page < kKeys ? page : kKeys, 1, 1};
     const int64_t qd[3] = {DIM, a.n_q_heads, a.n_tokens}, qs[3] = {1, DIM, a.q_stride};
     const int qb[3] = {64, group, p.tile_tokens};
-    if (!encode(&p.k_map, f16, a.kv.k, 4, kd, ks, kb) || !encode(&p.v_map, f16, a.kv.v, 4, kd, ks, kb) ||
-        !encode(&p.q_map, f16, a.q, 3, qd, qs, qb))
+    if (!encode_cache_maps(f16, a.kv, kKeys, &p.k_map, &p.v_map) || !encode(&p.q_map, f16, a.q, 3, qd, qs, qb))
         return cudaErrorInvalidValue;
     const int64_t items = tc_pairs(a.n_tokens, group, a.kv.n_seqs, prefix) * a.kv.n_heads * splits;
     return launch_serial(attn_tc_kernel<T, DIM>, dim3(unsigned(items < sm_count ? items : sm_count)), kTcThreads,
@@ -843,6 +827,14 @@ cudaError_t launch_tc(const AttnParams& a, bool prefix, int splits, float* part_
 }
 
 }  // namespace
+
+bool encode_cache_maps(bool f16, const KvView& kv, int keys, CUtensorMap* k, CUtensorMap* v) {
+    const int page = 1 << kv.page_shift;
+    const int64_t dims[4] = {kv.head_dim, page, kv.n_heads, kv.n_pages};
+    const int64_t strides[4] = {1, kv.slot_stride, kv.head_stride, kv.page_stride};
+    const int box[4] = {64, page < keys ? page : keys, 1, 1};
+    return encode(k, f16, kv.k, 4, dims, strides, box) && encode(v, f16, kv.v, 4, dims, strides, box);
+}
 
 // Tile pairs at most: each sequence may end with one that is not full.
 int64_t tc_pairs(int64_t n_tokens, int group, int n_seqs, bool prefix) {
