@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -391,25 +392,34 @@ def qx_gemv_chain_noalloc(jobs, stream=None, marshalled=None):
 _DTYPE = {torch.float32: QX_F32, torch.float16: QX_F16, torch.bfloat16: QX_BF16}
 
 
-def _dtype(t: torch.Tensor, what: str) -> int:
-    try:
-        return _DTYPE[t.dtype]
-    except KeyError:
-        raise TypeError(f"{what}: {t.dtype} is not float32, float16 or bfloat16") from None
+# These calls are short, so their marshalling is kept short too: the C structs
+# are packed as bytes in one step, and the current stream is asked for by its
+# number (torch.cuda.current_stream builds an object, 2 us).
+_PACK_QKV = struct.Struct("qiiPPPqqq")
+_PACK_NORM = struct.Struct("qqiiPPPPPffPPqqqqq")
+assert _PACK_QKV.size == ctypes.sizeof(_Qkv) and _PACK_NORM.size == ctypes.sizeof(_Norm)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _heads(t: torch.Tensor, heads: int, dim: int, tokens: int, dtype, what: str) -> int:
-    """Token stride of a [tokens, heads, dim] CUDA tensor whose heads of a token lie one after another."""
-    if not t.is_cuda:
-        raise ValueError("qx operates on CUDA tensors only")
+def _raw_stream(stream, index: int) -> int:
+    if stream is None:
+        return _current_raw_stream(index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _heads(t: torch.Tensor, shape: tuple, dtype, index: int, what: str) -> int:
+    """Token stride of a [tokens, heads, dim] tensor on GPU `index` whose heads of a token lie one after another."""
+    if t.get_device() != index:
+        raise ValueError(f"{what} is not on the cache's GPU" if t.is_cuda else "qx operates on CUDA tensors only")
     if t.dtype != dtype:
         raise TypeError(f"{what}: {t.dtype}, need {dtype}")
-    if t.shape != (tokens, heads, dim):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, need {(tokens, heads, dim)}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, need {shape}")
     a, b, c = t.stride()
-    if (c != 1 and dim > 1) or (b != dim and heads > 1):
+    if (c != 1 and shape[2] > 1) or (b != shape[2] and shape[1] > 1):
         raise ValueError(f"{what}: a token's heads must lie one after another (strides {(a, b, c)})")
-    return a if tokens > 1 else heads * dim
+    return a if shape[0] > 1 else shape[1] * shape[2]
 
 
 class PagedKV:
@@ -446,7 +456,7 @@ class PagedKV:
         if table.dim() != 2 or table.shape[0] != n or q_start.numel() != n + 1:
             raise ValueError("table [n_seqs, pages], kv_len [n_seqs] and q_start [n_seqs + 1] differ in n_seqs")
         self.k, self.v, self.table, self.kv_len, self.q_start = k, v, table, kv_len, q_start
-        self.dtype, self.device, self.n_seqs = k.dtype, k.device, n
+        self.dtype, self.device, self.n_seqs, self._index = k.dtype, k.device, n, k.get_device()
         pages, self.heads, self.page_size, self.head_dim = k.shape
         self._c = _Kv(k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], self.heads, self.head_dim, self.page_size, pages,
                       k.stride(0), k.stride(1), k.stride(2), table.data_ptr(), table.shape[1], kv_len.data_ptr(),
@@ -467,12 +477,6 @@ class PagedKV:
         return have[3]
 
 
-def _raw_stream(stream, device) -> int:
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
 def qx_rope_append(kv: PagedKV, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
                    cos: torch.Tensor | None = None, sin: torch.Tensor | None = None, interleaved: bool = False,
                    q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
@@ -481,50 +485,62 @@ def qx_rope_append(kv: PagedKV, q: torch.Tensor | None, k: torch.Tensor, v: torc
     cos, sin: float32 [positions, rot / 2] (None: no rotation); interleaved:
     pairs (2i, 2i + 1) instead of (i, i + rot / 2).  Returns the rotated
     queries in the cache's type."""
-    n, dim, dt = k.shape[0], kv.head_dim, k.dtype
-    code = _dtype(k, "k")
-    a = _Qkv(n, 0, code, None, k.data_ptr(), v.data_ptr(), 0, _heads(k, kv.heads, dim, n, dt, "k"),
-             _heads(v, kv.heads, dim, n, dt, "v"))
-    out = None
+    index, dim, dt = kv._index, kv.head_dim, k.dtype
+    code = _DTYPE.get(dt)
+    if code is None:
+        raise TypeError(f"k: {dt} is not float32, float16 or bfloat16")
+    n = k.shape[0]
+    own = (n, kv.heads, dim)
+    k_stride, v_stride = _heads(k, own, dt, index, "k"), _heads(v, own, dt, index, "v")
+    hq = q_ptr = q_stride = n_pos = half = 0
+    out = cp = sp = None
     if q is not None:
         hq = q.shape[1]
-        a.n_q_heads, a.q, a.q_stride = hq, q.data_ptr(), _heads(q, hq, dim, n, dt, "q")
+        q_stride, q_ptr = _heads(q, (n, hq, dim), dt, index, "q"), q.data_ptr()
         if q_out is None:
             q_out = torch.empty((n, hq, dim), dtype=kv.dtype, device=kv.device)
-        elif q_out.dtype != kv.dtype or q_out.shape != q.shape or not q_out.is_contiguous() or not q_out.is_cuda:
-            raise ValueError("q_out: need a contiguous CUDA tensor of q's shape and the cache's type")
+        elif q_out.dtype != kv.dtype or q_out.shape != q.shape or not q_out.is_contiguous() or q_out.get_device() != index:
+            raise ValueError("q_out: need a contiguous tensor on the cache's GPU, of q's shape and the cache's type")
         out = q_out.data_ptr()
-    cp = sp = None
-    n_pos = half = 0
     if cos is not None:
         if sin is None or cos.shape != sin.shape or cos.dim() != 2:
             raise ValueError("cos and sin need one shape [positions, rot / 2]")
         if cos.dtype != torch.float32 or sin.dtype != torch.float32:
             raise TypeError("cos and sin are float32")
+        if cos.get_device() != index or sin.get_device() != index or not cos.is_contiguous() or not sin.is_contiguous():
+            raise ValueError("cos and sin: need contiguous tensors on the cache's GPU")
         n_pos, half = cos.shape
-        cp, sp = _ptr(cos), _ptr(sin)
-    _check(lib().qx_rope_append(kv._ref, ctypes.byref(a), cp, sp, n_pos, 2 * half, 1 if interleaved else 0, out,
-                                _raw_stream(stream, kv.device)), "qx_rope_append")
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    a = _PACK_QKV.pack(n, hq, code, q_ptr, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride)
+    st = lib().qx_rope_append(kv._ref, a, cp, sp, n_pos, 2 * half, 1 if interleaved else 0, out, _raw_stream(stream, index))
+    if st:
+        _check(st, "qx_rope_append")
     return q_out
 
 
 def _attn(kv: PagedKV, q: torch.Tensor, scale, out, lse, stream):
-    if q.dim() != 3:
+    """The arguments before and after the mask's in the C calls."""
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q: need [tokens, heads, dim]")
-    n, hq, dim = q.shape
-    q_stride = _heads(q, hq, kv.head_dim, n, kv.dtype, "q")
+    n, hq, dim = shape
+    index = kv._index
+    q_stride = _heads(q, (n, hq, kv.head_dim), kv.dtype, index, "q")
     if out is None:
-        out = torch.empty((n, hq, dim), dtype=kv.dtype, device=kv.device)
-    elif out.shape != q.shape or not out.is_contiguous() or not out.is_cuda:
-        raise ValueError("out: need a contiguous CUDA tensor of q's shape")
+        out = torch.empty(shape, dtype=kv.dtype, device=kv.device)
+    elif out.shape != shape or not out.is_contiguous() or out.get_device() != index:
+        raise ValueError("out: need a contiguous tensor on the cache's GPU, of q's shape")
+    code = _DTYPE.get(out.dtype)
+    if code is None:
+        raise TypeError(f"out: {out.dtype} is not float32, float16 or bfloat16")
     lp = None
     if lse is not None:
         if lse.dtype != torch.float32:
             raise TypeError("lse is float32")
         lp = _ptr(_need(lse, n * hq * 4, "lse"))
-    s = _raw_stream(stream, kv.device)
+    s = _raw_stream(stream, index)
     return (kv._ref, q.data_ptr(), n, hq, q_stride, dim ** -0.5 if scale is None else scale), out, \
-        (out.data_ptr(), _dtype(out, "out"), lp, kv.scratch(n, hq, s), s)
+        (out.data_ptr(), code, lp, kv.scratch(n, hq, s), s)
 
 
 def qx_attn_paged(kv: PagedKV, q: torch.Tensor, scale: float | None = None, window: int = 0, sinks: int = 0,
@@ -535,7 +551,9 @@ def qx_attn_paged(kv: PagedKV, q: torch.Tensor, scale: float | None = None, wind
     `sinks`.  out: the cache's type or float32; lse: float32 [tokens, q_heads],
     filled with the rows' log-sum-exp."""
     head, out, tail = _attn(kv, q, scale, out, lse, stream)
-    _check(lib().qx_attn_paged(*head, window, sinks, *tail), "qx_attn_paged")
+    st = lib().qx_attn_paged(*head, window, sinks, *tail)
+    if st:
+        _check(st, "qx_attn_paged")
     return out
 
 
@@ -543,19 +561,35 @@ def qx_attn_shared(kv: PagedKV, q: torch.Tensor, shared_len: int, scale: float |
                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """qx_attn_paged for sequences that all begin with the same `shared_len` keys and values, read once for all."""
     head, out, tail = _attn(kv, q, scale, out, lse, stream)
-    _check(lib().qx_attn_shared(*head, shared_len, *tail), "qx_attn_shared")
+    st = lib().qx_attn_shared(*head, shared_len, *tail)
+    if st:
+        _check(st, "qx_attn_shared")
     return out
 
 
-def _rows(t: torch.Tensor, shape, what: str) -> int:
-    """Row stride of a [rows, cols] CUDA tensor with contiguous rows."""
-    if not t.is_cuda:
-        raise ValueError("qx operates on CUDA tensors only")
+def _rows(t: torch.Tensor, shape, dtype, index: int, what: str) -> int:
+    """Row stride of a [rows, cols] tensor on GPU `index` with contiguous rows."""
+    if t.get_device() != index:
+        raise ValueError(f"{what} is not on r's GPU" if t.is_cuda else "qx operates on CUDA tensors only")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {t.dtype}, need {dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, need {tuple(shape)}")
-    if t.stride(1) != 1 and shape[1] > 1:
+    a, b = t.stride()
+    if b != 1 and shape[1] > 1:
         raise ValueError(f"{what}: rows must be contiguous")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    return a if shape[0] > 1 else shape[1]
+
+
+def _vector(t: torch.Tensor, cols: int, dtype, index: int, what: str) -> int:
+    """Address of a contiguous vector of `cols` elements on GPU `index`."""
+    if t.get_device() != index:
+        raise ValueError(f"{what} is not on r's GPU" if t.is_cuda else "qx operates on CUDA tensors only")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {t.dtype}, need {dtype}")
+    if t.numel() != cols or not t.is_contiguous():
+        raise ValueError(f"{what}: need {cols} contiguous elements")
+    return t.data_ptr()
 
 
 def qx_block_norm(y: torch.Tensor | None, r: torch.Tensor, w_post: torch.Tensor | None = None,
@@ -567,48 +601,45 @@ def qx_block_norm(y: torch.Tensor | None, r: torch.Tensor, w_post: torch.Tensor 
     [cols] for all rows) and x share a type, r and r' another; w_post (None:
     y as it is) and w_pre (None: no x) are float32 [cols].  r_out may be r, and
     x_out may be y."""
-    if r.dim() != 2:
-        raise ValueError("r: need [rows, cols]")
     shape = r.shape
-    a = _Norm()
-    a.rows, a.cols = shape
-    act = y if y is not None else x_out
-    act_type = act.dtype if act is not None else r.dtype
-    a.dtype, a.res_dtype, a.alpha, a.eps = _DTYPE.get(act_type, -1), _DTYPE.get(r.dtype, -1), alpha, eps
-    if a.dtype < 0 or a.res_dtype < 0:
+    if len(shape) != 2:
+        raise ValueError("r: need [rows, cols]")
+    index, res, cols = r.get_device(), r.dtype, shape[1]
+    if index < 0:
+        raise ValueError("qx operates on CUDA tensors only")
+    act = y.dtype if y is not None else x_out.dtype if x_out is not None else res
+    code, res_code = _DTYPE.get(act), _DTYPE.get(res)
+    if code is None or res_code is None:
         raise TypeError("qx_block_norm takes float32, float16 and bfloat16")
-    a.r, a.r_stride = r.data_ptr(), _rows(r, shape, "r")
+    r_stride = _rows(r, shape, res, index, "r")
+    y_ptr = gate_ptr = post = pre = ro_ptr = x_ptr = y_stride = gate_stride = ro_stride = x_stride = 0
     if y is not None:
-        a.y, a.y_stride = y.data_ptr(), _rows(y, shape, "y")
+        y_ptr, y_stride = y.data_ptr(), _rows(y, shape, act, index, "y")
     if gate is not None:
-        if gate.dtype != act_type:
-            raise TypeError("gate has y's type")
         if gate.dim() == 1:
-            a.gate, a.gate_stride = _ptr(_need(gate, shape[1] * gate.element_size(), "gate")), 0
+            gate_ptr = _vector(gate, cols, act, index, "gate")
         else:
-            a.gate, a.gate_stride = gate.data_ptr(), _rows(gate, shape, "gate")
-    for w, what in ((w_post, "w_post"), (w_pre, "w_pre")):
-        if w is not None:
-            if w.dtype != torch.float32:
-                raise TypeError(f"{what} is float32")
-            setattr(a, what, _ptr(_need(w, shape[1] * 4, what)))
+            gate_ptr, gate_stride = gate.data_ptr(), _rows(gate, shape, act, index, "gate")
+    if w_post is not None:
+        post = _vector(w_post, cols, torch.float32, index, "w_post")
     if y is None and r_out is None:
-        r_out = r
+        r_out = r  # unchanged
     else:
         if r_out is None:
-            r_out = torch.empty_like(r, memory_format=torch.contiguous_format)
-        elif r_out.dtype != r.dtype:
-            raise TypeError("r_out has r's type")
-        a.r_out, a.r_out_stride = r_out.data_ptr(), _rows(r_out, shape, "r_out")
+            r_out = torch.empty(shape, dtype=res, device=r.device)
+        ro_ptr, ro_stride = r_out.data_ptr(), _rows(r_out, shape, res, index, "r_out")
     if w_pre is not None:
+        pre = _vector(w_pre, cols, torch.float32, index, "w_pre")
         if x_out is None:
-            x_out = torch.empty(shape, dtype=act_type, device=r.device)
-        elif x_out.dtype != act_type:
-            raise TypeError("x_out has y's type")
-        a.x, a.x_stride = x_out.data_ptr(), _rows(x_out, shape, "x_out")
+            x_out = torch.empty(shape, dtype=act, device=r.device)
+        x_ptr, x_stride = x_out.data_ptr(), _rows(x_out, shape, act, index, "x_out")
     else:
         x_out = None
-    _check(lib().qx_block_norm(ctypes.byref(a), _raw_stream(stream, r.device)), "qx_block_norm")
+    a = _PACK_NORM.pack(shape[0], cols, code, res_code, y_ptr, r.data_ptr(), gate_ptr, post, pre, alpha, eps, ro_ptr, x_ptr, y_stride,
+                        r_stride, gate_stride, ro_stride, x_stride)
+    st = lib().qx_block_norm(a, _raw_stream(stream, index))
+    if st:
+        _check(st, "qx_block_norm")
     return r_out, x_out
 
 
