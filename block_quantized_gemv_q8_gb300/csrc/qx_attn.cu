@@ -138,9 +138,8 @@ struct SplitGeom {
     static constexpr int kPanelBytes = kUnit * 128;
     static constexpr int kHalfStage = kPanels * kPanelBytes;  // a unit's keys; its values follow
     static constexpr int kStages = kRingBytes / (2 * kHalfStage);
-    static constexpr int kPad = DIM + 4;  // floats of a row in the joining buffer: 8 rows of each warp, then their m and l
-    static constexpr int kJoin = (kSplitWarps * 8 * (kPad + 2)) * 4;
-    static constexpr int kMisc = 256;     // barriers, the worker's place on the line
+    static constexpr int kJoin = (kSplitWarps * 8 * (DIM + 2)) * 4;  // joining buffer: 8 rows of each warp, then their m and l
+    static constexpr int kMisc = 640;     // barriers, what is known of each unit, the worker's place on the line
     static constexpr size_t kSmem = kRingBytes + kJoin + kMisc;
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 };
@@ -240,6 +239,18 @@ __device__ __forceinline__ int unit_keys(const SeqWork& w, int u, int& lo, int& 
     return (sink ? u : w.lo / kUnit + (u - w.sink_units)) * kUnit;
 }
 
+// What the consumers are told of a unit, beside its keys and values in the
+// ring: its first key and the keys [lo, hi) that any row sees; the tile's
+// rows; and the workers that share the tile.
+struct UnitInfo {
+    int j0, lo, hi;
+    int flags;           // kSink, kOpens, kCloses (for this worker)
+    int t0, r0, rows;    // the sequence's first token, the tile's first row and the rows from it on
+    int hk, pos0;
+    int wf, parts, part; // first worker, workers after it, and the part of the scratch that the first one writes
+};
+constexpr int kSink = 1, kOpens = 2, kCloses = 4;
+
 struct SplitParams {
     CUtensorMap k_map;  // [pages][heads][slots][dim], boxes of min(page, 64) keys x 64
     CUtensorMap v_map;
@@ -263,14 +274,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     constexpr int NS = G::kStages;
     const AttnParams& p = pp.a;
     extern __shared__ __align__(1024) uint8_t smem[];
-    float* buf = reinterpret_cast<float*>(smem + kRingBytes);  // [4 warps][8 rows][kPad], then m and l of each
-    float* buf_ml = buf + kSplitWarps * 8 * G::kPad;
+    float* buf = reinterpret_cast<float*>(smem + kRingBytes);  // [4 warps][8 rows][DIM], then m and l of each
+    float* buf_ml = buf + kSplitWarps * 8 * DIM;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes + G::kJoin);
     uint64_t* empty = full + NS;
     int64_t* scan = reinterpret_cast<int64_t*>(empty + NS);  // [5]
     Cursor* start = reinterpret_cast<Cursor*>(scan + kSplitWarps + 1);
-    int* last_flag = reinterpret_cast<int*>(start + 1);
-    static_assert((2 * NS + kSplitWarps + 1) * 8 + sizeof(Cursor) + 4 <= G::kMisc, "barriers and the worker's place");
+    UnitInfo* info = reinterpret_cast<UnitInfo*>(start + 1);  // [NS], and the first unit's
+    int* last_flag = reinterpret_cast<int*>(info + NS + 1);
+    static_assert((2 * NS + kSplitWarps + 1) * 8 + sizeof(Cursor) + (NS + 1) * sizeof(UnitInfo) + 4 <= G::kMisc,
+                  "barriers, units and the worker's place");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -341,12 +354,30 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         }
     }
     __syncthreads();
-    Cursor cur = *start;
-    int ui = int(first - cur.begin);  // unit of the tile
-    int64_t left = last - first;      // units to go
+    int64_t left = last - first;  // units to go
+    const auto describe = [&](const Cursor& c, int u, UnitInfo& x) {
+        x.j0 = unit_keys(c.w, u, x.lo, x.hi);
+        const int64_t begin = c.begin, end = c.begin + c.w.units, here = begin + u;
+        x.flags = (u < c.w.sink_units ? kSink : 0) | (here == first || u == 0 ? kOpens : 0) | (here + 1 == last || here + 1 == end ? kCloses : 0);
+        x.t0 = c.w.t0;
+        x.r0 = kRows * c.rt;
+        x.rows = c.w.tokens * group - x.r0;
+        x.hk = c.hk;
+        x.pos0 = c.w.pos0;
+        // only a worker's first and last tile may be shared; its part of a
+        // tile lies in its first slot, or in its second where another tile's
+        // end came first
+        const int64_t wf = begin < first ? worker_of(begin) : blockIdx.x, wl = end > last ? worker_of(end - 1) : blockIdx.x;
+        x.wf = int(wf);
+        x.parts = int(wl - wf);
+        x.part = 2 * int(wf) + (begin_of(wf) < begin ? 1 : 0);
+    };
+    if (threadIdx.x == 0) describe(*start, int(first - start->begin), info[NS]);
 
     if (warp == kSplitWarps) {
         // ---- producer: a lane for each page of a unit
+        Cursor cur = *start;
+        int ui = int(first - cur.begin);  // unit of the tile
         const int page_keys = (1 << p.kv.page_shift) < kUnit ? (1 << p.kv.page_shift) : kUnit;
         const int in_page_mask = (1 << p.kv.page_shift) - 1;
         const int boxes = kUnit / page_keys;  // at most 4
@@ -365,6 +396,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
             int lo, hi;
             const int j0 = unit_keys(cur.w, ui, lo, hi);
             const int in_page = (j0 + lane * page_keys) & in_page_mask, hk = cur.hk, now = page;
+            UnitInfo x;
+            describe(cur, ui, x);
             if (left > 1) {  // the next unit's pages are looked up while this one's room is awaited
                 if (++ui == cur.w.units) {
                     next_tile(p, cur, group);
@@ -375,7 +408,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
             const unsigned live = __ballot_sync(0xffffffffu, now >= 0);
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[slot], phase, kSplitWaitNs, p.kv.err, kErrTimeoutEmpty));
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(live) * page_keys * 128 * G::kPanels * 2);
+            if (lane == 0) {
+                info[slot] = x;
+                mbar_arrive_expect_tx(&full[slot], __popc(live) * page_keys * 128 * G::kPanels * 2);
+            }
             __syncwarp();
             if (now >= 0) {
                 uint8_t* dst = smem + slot * 2 * G::kHalfStage + lane * page_keys * 128;
@@ -411,18 +447,18 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     int rpos[2];             // positions of this lane's two rows (-1: none)
     int pos_first, pos_last; // of the tile's rows
     // A tile's rows: 16 rt + lane / 4 and eight further.
-    const auto open_tile = [&](const Cursor& c) {
-        const int rows = c.w.tokens * group, r0 = kRows * c.rt;
-        pos_first = c.w.pos0 + r0 / group;
-        pos_last = c.w.pos0 + (r0 + kRows < rows ? r0 + kRows - 1 : rows - 1) / group;
+    const auto open_tile = [&](const UnitInfo& x) {
+        const int live_rows = x.rows < kRows ? x.rows : kRows;
+        pos_first = x.pos0 + x.r0 / group;
+        pos_last = x.pos0 + (x.r0 + live_rows - 1) / group;
         if (pos_last < -1) pos_last = -1;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int r = r0 + (lane >> 2) + 8 * i;
-            const bool live = r < rows;
-            const int tok = live ? r / group : 0, g = live ? r - tok * group : 0;
-            rpos[i] = live && c.w.pos0 + tok >= 0 ? c.w.pos0 + tok : -1;
-            const T* q = static_cast<const T*>(p.q) + int64_t(c.w.t0 + tok) * p.q_stride + int64_t(c.hk * group + g) * DIM + 2 * (lane & 3);
+            const int r = (lane >> 2) + 8 * i;
+            const bool live = r < live_rows;
+            const int tok = (x.r0 + (live ? r : 0)) / group, g = x.r0 + (live ? r : 0) - tok * group;
+            rpos[i] = live && x.pos0 + tok >= 0 ? x.pos0 + tok : -1;
+            const T* q = static_cast<const T*>(p.q) + int64_t(x.t0 + tok) * p.q_stride + int64_t(x.hk * group + g) * DIM + 2 * (lane & 3);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 qf[k][i] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
@@ -430,7 +466,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
             }
         }
     };
-    open_tile(cur);
+    consumers_sync();  // the first unit's description
+    open_tile(info[NS]);
     float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(p.scratch) + kCounterBytes);
     unsigned* counters = static_cast<unsigned*>(p.scratch);
     const int window = p.window > 0 && p.window < INT32_MAX ? int(p.window) : INT32_MAX;
@@ -444,19 +481,21 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     const uint32_t k_row = ring + kr * 128, v_row = ring + G::kHalfStage + vr * 128;
     int slot = 0;
     uint32_t phase = 0;
-    bool fresh = true, ok = true;
+    bool ok = true;
+    // (after a wait that ran out the rest runs through without waiting, for the barriers' sake)
+    const auto arrived = [&]() {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], phase, kSplitWaitNs, p.kv.err, kErrTimeoutFull));
+    };
+    arrived();
     for (; left > 0; --left) {
-        if (fresh) {
+        const int flags = info[slot].flags, lo = info[slot].lo, hi = info[slot].hi;
+        const int j0 = info[slot].j0 + 16 * warp;  // this warp's sixteen keys
+        if (flags & kOpens) {
             m[0] = m[1] = -INFINITY;
             l[0] = l[1] = 0.0f;
 #pragma unroll
             for (int d = 0; d < DIM / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.0f;
-            fresh = false;
         }
-        int lo, hi;
-        const int j0 = unit_keys(cur.w, ui, lo, hi) + 16 * warp;  // this warp's sixteen keys
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], phase, kSplitWaitNs, p.kv.err, kErrTimeoutFull));
-        if (!ok) break;
         if (j0 + 16 > lo && j0 < hi) {
             const uint32_t off = slot * 2 * G::kHalfStage;
             float s[2][4] = {};
@@ -471,7 +510,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[n][e] *= p.scale_log2;
-            const bool sink_unit = ui < cur.w.sink_units;
+            const bool sink_unit = flags & kSink;
             if (j0 < lo || j0 + 16 > hi || j0 + 15 > pos_first || (!sink_unit && pos_last - window >= j0)) {
                 // some row does not see some of them.  This lane's keys,
                 // relative to the first: 2 (lane % 4) + {0, 1, 8, 9}.
@@ -543,34 +582,27 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                 mma16816<T>(o[2 * k + 1], pf, b[2], b[3]);
             }
         }
+        const UnitInfo* const x = &info[slot];
+        UnitInfo done;
+        if (flags & kCloses) done = *x;
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
         if (++slot == NS) {
             slot = 0;
             phase ^= 1;
         }
-        if (++ui < cur.w.units && left > 1) continue;
+        if (left > 1) arrived();
+        if (!(flags & kCloses)) continue;
         // ---- the tile ends here (for this worker).  The next one's queries
         // are on their way while its warps are joined, eight rows at a time:
         // every warp leaves its (m, l, o), and every thread then joins some
         // elements.
-        const int rt = cur.rt, hk = cur.hk, t0 = cur.w.t0;
-        const int rows = cur.w.tokens * group - kRows * rt;  // of this tile (16 at most count)
-        const int64_t t_begin = cur.begin, t_end = cur.begin + cur.w.units;
-        if (left > 1) {
-            next_tile(p, cur, group);
-            open_tile(cur);
-            ui = 0;
-            fresh = true;
-        }
-        const int64_t wf = worker_of(t_begin), wl = worker_of(t_end - 1);  // the first and last worker of the tile
-        // A worker's part of a tile lies in its first slot, or in its second
-        // where another tile's end came first.
-        const auto slot_of = [&](int64_t w) -> float* { return partials + 2 * w * partial_floats<DIM>(); };
-        float* const wf_slot = slot_of(wf) + (begin_of(wf) < t_begin ? partial_floats<DIM>() : 0);
+        if (left > 1) open_tile(info[slot]);
+        const int rows = done.rows;  // (16 at most count)
+        const auto part_at = [&](int i) -> float* { return partials + int64_t(i) * partial_floats<DIM>(); };
         const auto finish = [&](int r, int d, float M, float L, float4 v) {
-            const int rr = kRows * rt + r;
-            const int64_t row = int64_t(t0 + rr / group) * p.n_q_heads + hk * group + rr % group;
+            const int rr = done.r0 + r;
+            const int64_t row = int64_t(done.t0 + rr / group) * p.n_q_heads + done.hk * group + rr % group;
             const float inv = L > 0.0f ? 1.0f / L : 0.0f;
             v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
             if (pp.part_o) {
@@ -590,9 +622,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
             if (i > 0) consumers_sync();  // the first eight are read
             if ((lane >> 2) < live) {
-                float* row = buf + (8 * warp + (lane >> 2)) * G::kPad + 2 * (lane & 3);
+                // (groups of eight elements permuted by the row, for the banks)
+                float* row = buf + (8 * warp + (lane >> 2)) * DIM + 2 * (lane & 3);
 #pragma unroll
-                for (int d = 0; d < DIM / 8; ++d) *reinterpret_cast<float2*>(row + 8 * d) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
+                for (int d = 0; d < DIM / 8; ++d)
+                    *reinterpret_cast<float2*>(row + 8 * (d ^ (lane >> 2))) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
                 if ((lane & 3) == 0) *reinterpret_cast<float2*>(buf_ml + 2 * (8 * warp + (lane >> 2))) = make_float2(m[i], l[i]);
             }
             consumers_sync();
@@ -609,40 +643,42 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
 #pragma unroll
                 for (int w = 0; w < kSplitWarps; ++w) {
                     const float a = ml[w].x == -INFINITY ? 0.0f : exp2_approx(ml[w].x - M);
-                    const float4 v = *reinterpret_cast<const float4*>(buf + (8 * w + r) * G::kPad + d);
+                    const float4 v = *reinterpret_cast<const float4*>(buf + (8 * w + r) * DIM + (d ^ (8 * r)));
                     L += a * ml[w].y;
                     acc.x += a * v.x, acc.y += a * v.y, acc.z += a * v.z, acc.w += a * v.w;
                 }
-                if (wf == wl) {
+                if (done.parts == 0) {
                     finish(8 * i + r, d, M, L, acc);
                 } else {
-                    float* to = (blockIdx.x == wf ? wf_slot : slot_of(blockIdx.x));
+                    float* to = part_at(int(blockIdx.x) == done.wf ? done.part : 2 * int(blockIdx.x));
                     *reinterpret_cast<float4*>(to + (8 * i + r) * DIM + d) = acc;
                     if (d == 0) *reinterpret_cast<float2*>(to + kRows * DIM + 2 * (8 * i + r)) = make_float2(M, L);
                 }
             }
         }
-        if (wf != wl) {
+        if (done.parts > 0) {
             // ---- this worker's part is written; the last to arrive joins all
-            __threadfence();
             consumers_sync();
             if (threadIdx.x == 0) {
-                const unsigned n = atomicAdd(&counters[wf], 1u);
-                *last_flag = n == unsigned(wl - wf);
-                if (*last_flag) counters[wf] = 0;  // for the next call
+                __threadfence();  // for all, behind the barrier
+                const unsigned n = atomicAdd(&counters[done.wf], 1u);
+                *last_flag = n == unsigned(done.parts);
+                if (*last_flag) {
+                    counters[done.wf] = 0;  // for the next call
+                    __threadfence();
+                }
             }
             consumers_sync();
             if (*last_flag) {
-                __threadfence();
-                const int live = rows < kRows ? rows : kRows, parts = int(wl - wf);  // beyond the first
-                const float* rest = slot_of(wf + 1);
+                const int live = rows < kRows ? rows : kRows, parts = done.parts;  // beyond the first
+                const float *begin = part_at(done.part), *rest = part_at(2 * (done.wf + 1));
                 constexpr int64_t kStep = 2 * partial_floats<DIM>();
                 for (int x = threadIdx.x; x < live * (DIM / 4); x += 32 * kSplitWarps) {
                     const int r = x / (DIM / 4), d = x % (DIM / 4) * 4;
                     const int at_ml = kRows * DIM + 2 * r, at_o = r * DIM + d;
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(wf_slot + at_ml));
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(begin + at_ml));
                     float M = ml.x, L = ml.y;
-                    float4 acc = __ldcg(reinterpret_cast<const float4*>(wf_slot + at_o));
+                    float4 acc = __ldcg(reinterpret_cast<const float4*>(begin + at_o));
                     // eight parts' loads in flight at a time
                     for (int w0 = 0; w0 < parts; w0 += 8) {
                         float2 e[8];

@@ -249,11 +249,13 @@ struct NormParams {
     int64_t rows;
     int cols;
     float alpha, eps;
+    int stages;    // rows in the ring (block_norm_rows_kernel)
+    unsigned* err; // device error word
 };
 
 cudaError_t launch_rope(int src, int dst, const RopeParams& p, int sm_count, cudaStream_t s);
 cudaError_t launch_attn(int dtype, const AttnParams& p, int sm_count, cudaStream_t s);
 size_t attn_scratch_bytes(int64_t n_tokens, int n_q_heads, int n_heads, int head_dim, int n_seqs);
-cudaError_t launch_norm(int dtype, int res_dtype, const NormParams& p, bool vec, cudaStream_t s);
+cudaError_t launch_norm(int dtype, int res_dtype, const NormParams& p, bool vec, int sm_count, cudaStream_t s);
 
 }  // namespace qx

@@ -190,11 +190,12 @@ qx_status qx_block_norm(const qx_norm_args* a, qx_stream_t s) {
     p.cols = int(a->cols);
     p.alpha = a->alpha;
     p.eps = a->eps;
+    p.err = err;
     // 16-byte access: whole vectors of eight in every row of every operand.
     const bool vec = a->cols % 8 == 0 && on16(a->y) && on16(a->r) && on16(a->gate) && on16(a->w_post) &&
                      on16(a->w_pre) && on16(a->r_out) && on16(a->x) && a->y_stride % 8 == 0 && a->r_stride % 8 == 0 &&
                      a->gate_stride % 8 == 0 && a->r_out_stride % 8 == 0 && a->x_stride % 8 == 0;
-    return report_cuda(launch_norm(a->dtype, a->res_dtype, p, vec, reinterpret_cast<cudaStream_t>(s)), "norm launch");
+    return report_cuda(launch_norm(a->dtype, a->res_dtype, p, vec, sms, reinterpret_cast<cudaStream_t>(s)), "norm launch");
 }
 
 }  // extern "C"

@@ -412,6 +412,24 @@ def test_block_norm(act, res, rows, cols):
         check_norm(y, r, w1 if post else None, gate, alpha, w2 if pre else None, 1e-6, r2, x)
 
 
+@pytest.mark.parametrize("act,res", [(F32, F32), (BF16, F32), (F16, BF16)])
+@pytest.mark.parametrize("rows,cols", [(3000, 4096), (700, 8192), (6000, 96), (2500, 1000), (1300, 4104)])
+def test_block_norm_of_many_rows(act, res, rows, cols):
+    """More rows than the GPU holds at a time, in every combination of operands."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    make = lambda *shape, dt=F32, std=1.0: torch.empty(shape, dtype=dt, device="cuda").normal_(0, std, generator=g)  # noqa: E731
+    y, r, w1, w2 = make(rows, cols, dt=act), make(rows, cols, dt=res, std=2.0), make(cols), make(cols)
+    some = torch.randperm(rows, generator=g, device="cuda")[:40]
+    for gate in (None, make(cols, dt=act), make(rows, cols, dt=act)):
+        for post, pre in ((w1, w2), (None, w2), (w1, None)):
+            r2, x = qx.qx_block_norm(y, r, w_post=post, gate=gate, alpha=0.7, w_pre=pre)
+            part = gate if gate is None or gate.dim() == 1 else gate[some]
+            check_norm(y[some], r[some], post, part, 0.7, pre, 1e-5, r2[some], None if pre is None else x[some])
+    r2, x = qx.qx_block_norm(None, r, w_pre=w2, r_out=torch.empty_like(r), x_out=torch.empty(rows, cols, dtype=act, device="cuda"))
+    check_norm(None, r[some], None, None, 1.0, w2, 1e-5, r2[some], x[some])
+    assert qx.qx_device_check() == qx.QX_OK
+
+
 def check_norm(y, r, w_post, gate, alpha, w_pre, eps, r2, x):
     torch.cuda.synchronize()
     host = [None if t is None else ref.f64(t) for t in (y, r, w_post, gate, w_pre)]
