@@ -93,11 +93,11 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_row_kernel(const __grid_c
         L += a[w] * ol[w];
     }
     const int64_t row = int64_t(t) * p.n_q_heads + h;
-    if (p.lse && threadIdx.x == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    if (p.lse && threadIdx.x == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     for (int d = threadIdx.x; d < dim; d += 32 * kRowWarps) {
         float v = 0.0f;
         for (int w = 0; w < kRowWarps; ++w) v += a[w] * oo[w][d];
-        v = L > 0.0f ? v / L : 0.0f;
+        v = L == 0.0f ? 0.0f : v / L;
         if (p.out_f32) static_cast<float*>(p.out)[row * dim + d] = v;
         else static_cast<T*>(p.out)[row * dim + d] = from_f32<T>(v);
     }
@@ -603,16 +603,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         const auto finish = [&](int r, int d, float M, float L, float4 v) {
             const int rr = done.r0 + r;
             const int64_t row = int64_t(done.t0 + rr / group) * p.n_q_heads + done.hk * group + rr % group;
-            const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
             if (pp.part_o) {
                 *reinterpret_cast<float4*>(pp.part_o + row * DIM + d) = v;
-                if (d == 0) pp.part_lse[row] = L > 0.0f ? M + log2f(L) : -INFINITY;
+                if (d == 0) pp.part_lse[row] = L == 0.0f ? -INFINITY : M + log2f(L);
                 return;
             }
             if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * DIM + d) = v;
             else *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * DIM + d) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
-            if (p.lse && d == 0) p.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+            if (p.lse && d == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
         };
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -747,19 +747,28 @@ cudaError_t launch_row(const AttnParams& p, cudaStream_t s) {
 }
 
 constexpr size_t kSplitScratch = kCounterBytes + size_t(kMaxWorkers) * 2 * partial_floats<128>() * 4;
-// Rows of parts that the scratch holds: enough to split the keys of few rows
-// over the GPU, and two parts of any call whose shared prefix is taken apart.
-constexpr int64_t kPartRows = 65536, kMaxSharedRows = 131072;
-int64_t part_rows(int64_t rows) {
-    const int64_t two = 2 * (rows < kMaxSharedRows ? rows : kMaxSharedRows);
-    return two > kPartRows ? (two + 63) / 64 * 64 : kPartRows;  // 256-byte multiples
-}
+// Rows of parts that the scratch holds for a call of `rows` rows: every row
+// split kMaxSplits ways, but no more than kPartRows rows in all (calls of that
+// many rows fill the GPU without splitting their keys), or two parts of a call
+// whose shared prefix is taken apart.
 constexpr int kMaxSplits = 31;  // of one launch: with the tails' part a row has at most 32
+constexpr int64_t kPartRows = 196608, kMaxSharedRows = 131072;
+int64_t part_rows(int64_t rows) {
+    int64_t n = rows < kPartRows / kMaxSplits ? rows * kMaxSplits : kPartRows;
+    const int64_t two = 2 * (rows < kMaxSharedRows ? rows : kMaxSharedRows);
+    if (n < two) n = two;
+    return (n + 63) / 64 * 64;  // 256-byte multiples
+}
 
-// CTAs that share a tile pair's keys: as many as give every SM one.
-int splits_for(int64_t ctas, int64_t rows, int64_t spare_rows, int sm_count) {
-    int64_t n = ctas > 0 ? sm_count / ctas : 1;
+// CTAs that share a tile pair's keys: as many as give every SM one, where the
+// pairs alone do not.  (More parts than SMs cost more than their better balance
+// gains, since each is written and read in f32: a chunk of 512 tokens over
+// 16384 keys, 64 pairs, took 115 us with 2 parts each and 122 with 7; 4096
+// causal tokens, 512 pairs, 107 us with one and 164 with two.)
+int splits_for(int64_t pairs, int64_t blocks, int64_t rows, int64_t spare_rows, int sm_count) {
+    int64_t n = sm_count / (pairs > 0 ? pairs : 1);
     if (n > kMaxSplits) n = kMaxSplits;
+    if (n > blocks) n = blocks;
     if (n * rows > spare_rows) n = spare_rows / rows;
     return n < 1 ? 1 : int(n);
 }
@@ -795,10 +804,11 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
     j.part_lse = part_lse;
     j.parts = 0;
     cudaError_t e;
-    int64_t spare = part_rows(rows);
+    const int64_t spare = part_rows(rows);
     if (p.shared_len > 0) {
-        spare -= rows;  // the tails' part
-        j.parts = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, true) * p.kv.n_heads, rows, spare, sm_count);
+        // the prefix, the tails beside it, and both joined
+        j.parts = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, true) * p.kv.n_heads, (p.shared_len + 127) / 128, rows, spare - rows,
+                             sm_count);
         if ((e = launch_attn_tc(dtype, p, true, j.parts, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
         float* o = part_o + j.parts * rows * dim;
         float* l = part_lse + j.parts * rows;
@@ -807,7 +817,9 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
         return e != cudaSuccess ? e : launch_attn_join(dtype, j, s);
     }
     if (!many) return launch_split_any(dtype, p, nullptr, nullptr, false, sm_count, s);
-    const int n = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, false) * p.kv.n_heads, rows, spare, sm_count);
+    int64_t keys = p.kv.table_stride << p.kv.page_shift;
+    if (p.window > 0 && p.window + 256 < keys) keys = p.window + 256;
+    const int n = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, false) * p.kv.n_heads, (keys + 127) / 128, rows, spare, sm_count);
     if (n == 1) return launch_attn_tc(dtype, p, false, 1, nullptr, nullptr, counter, sm_count, s);
     if ((e = launch_attn_tc(dtype, p, false, n, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
     j.parts = n;

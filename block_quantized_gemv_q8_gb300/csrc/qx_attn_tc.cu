@@ -53,6 +53,8 @@ constexpr int kTcThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "registers the CTA was launched with");
 constexpr float kRescale = 8.0f;
+constexpr int kMinPart = 8;            // blocks: a part costs some 5 us beside them
+constexpr float kWritten = INFINITY;   // as a row's first base-2 log: the row is in the output already
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 template <int DIM>
@@ -60,8 +62,8 @@ struct TcGeom {
     static constexpr int kPanels = DIM / 64;                    // 64 elements (128 bytes) of every row
     static constexpr int kPanelBytes = 128 * 128;               // 128 rows
     static constexpr int kTileBytes = kPanels * kPanelBytes;    // Q of a tile, or a block's K or V
-    static constexpr int kSlots = DIM == 128 ? 5 : 10;          // ring of K and V blocks
-    static constexpr size_t kSmem = size_t(2 + kSlots) * kTileBytes + 1024 + 512;
+    static constexpr int kSlots = DIM == 128 ? 4 : 10;          // ring of K and V blocks
+    static constexpr size_t kSmem = size_t(2 + kSlots) * kTileBytes + kSoftmaxWarps * 4096 + 1024 + 640;
 };
 static_assert(TcGeom<128>::kSmem <= 227 * 1024 && TcGeom<64>::kSmem <= 227 * 1024, "a CTA's shared memory");
 
@@ -73,6 +75,7 @@ struct TcAttnParams {
     int tile_tokens;    // tokens of a tile: 128 / group
     int splits;         // CTAs that share a tile pair's keys
     int prefix;         // 1: every token against keys [0, shared_len)
+    int tails;          // 1: the parts of a call whose prefix is taken apart
     float* part_o;      // parts: [splits][tokens * heads][dim], or null: write the output
     float* part_lse;    // [splits][tokens * heads]
     unsigned* counter;  // pairs taken beyond each CTA's first, and CTAs done; zero between calls
@@ -165,12 +168,61 @@ __device__ __forceinline__ uint32_t bits_from(int n) {
     return r;
 }
 
+// A warp's rows of O (one a lane, in tensor memory at `o`; null rows where
+// nothing was summed up) times `inv`, to element `at` of `dst`, through 4 KB
+// of shared memory: 128 bytes of every row at a time, so that eight lanes
+// write a row's 128 bytes together.  (Each lane writing its own row made 32
+// lines of every store: the epilogue took 8000 cycles, and the MMA issuer's
+// barrier accesses stood behind it.)  `left`: told when O has been read.
+template <int DIM, typename T>
+__device__ __forceinline__ void write_rows(T* dst, int64_t at, bool live, uint32_t o, bool some, float inv, uint8_t* stage, int lane,
+                                           uint64_t* left) {
+    constexpr int E = 128 / int(sizeof(T));  // elements a pass
+    if (!live) at = -1;
+#pragma unroll
+    for (int x0 = 0; x0 < DIM; x0 += E) {
+        float v[E];
+#pragma unroll
+        for (int x = 0; x < E; ++x) v[x] = 0.0f;
+        if (some) {
+#pragma unroll
+            for (int x = 0; x < E; x += 32) ld32(o + x0 + x, v + x);
+            wait_ld();
+            if (x0 + E >= DIM) {
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(left);
+            }
+        }
+        __syncwarp();  // the pass before is read
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint32_t u[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if constexpr (sizeof(T) == 4) u[x] = __float_as_uint(v[4 * c + x] * inv);
+                else u[x] = pack2<T>(v[8 * c + 2 * x] * inv, v[8 * c + 2 * x + 1] * inv);
+            }
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + (lane >> 3), c = lane & 7;
+            const int64_t to = __shfl_sync(0xffffffffu, at, r);
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+            if (to >= 0) *reinterpret_cast<uint4*>(dst + to + x0 + c * (E / 8)) = w;
+        }
+    }
+}
+
 // What a CTA works on: `tokens` tokens from t0 on (at most two tiles) of
 // sequence b, the first at position pos0, and the key blocks that any of its
 // rows sees: those of keys [0, sinks), then those of [lo, end).
 struct TcWork {
     int b, t0, tokens, pos0, lo, end, sinks, sink_blocks, blocks;
     int hk, split, i0, nb;  // key head, part, and its blocks [i0, i0 + nb)
+    int parts;              // parts that have blocks
 };
 __device__ __forceinline__ int key_block(const TcWork& w, int i) {  // first key of the i-th block
     return (i < w.sink_blocks ? i : w.lo / kKeys + (i - w.sink_blocks)) * kKeys;
@@ -297,7 +349,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     uint8_t* sq = smem;                        // [2 tiles][panels][128 rows][128 B]
     uint8_t* ring = sq + 2 * G::kTileBytes;    // [NS] blocks: K0, V0, K1, V1, ... of pair after pair
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(ring + NS * G::kTileBytes);
+    uint8_t* outs = ring + NS * G::kTileBytes;  // 4 KB for each softmax warp's rows on their way out
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(outs + kSoftmaxWarps * 4096);
     uint64_t* q_empty = q_full + 1;
     uint64_t* kv_full = q_empty + 1;
     uint64_t* kv_empty = kv_full + NS;
@@ -310,7 +363,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     uint64_t* w_empty = w_full + 2;
     TcWork* work = reinterpret_cast<TcWork*>(w_empty + 2);  // [2]: pairs in hand; tokens 0: no more
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(work + 2);
-    static_assert((2 + 3 * NS + 2 + 4 + 2 + 2 + 2 + 2) * 8 + 2 * sizeof(TcWork) + 4 <= 512, "barriers and work entries");
+    static_assert((2 + 3 * NS + 2 + 4 + 2 + 2 + 2 + 2) * 8 + 2 * sizeof(TcWork) + 4 <= 640, "barriers and work entries");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KvView& kv = p.a.kv;
@@ -375,8 +428,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 if (!more) w.tokens = 0;
                 w.hk = rest / p.splits;
                 w.split = rest - w.hk * p.splits;
-                w.i0 = more ? int(int64_t(w.blocks) * w.split / p.splits) : 0;
-                w.nb = more ? int(int64_t(w.blocks) * (w.split + 1) / p.splits) - w.i0 : 0;
+                // parts of at least kMinPart blocks; the others are empty
+                w.parts = more ? w.blocks / kMinPart : 1;
+                w.parts = w.parts < 1 ? 1 : w.parts < p.splits ? w.parts : p.splits;
+                const bool in = more && w.split < w.parts;
+                w.i0 = in ? int(int64_t(w.blocks) * w.split / w.parts) : 0;
+                w.nb = in ? int(int64_t(w.blocks) * (w.split + 1) / w.parts) - w.i0 : 0;
                 if (lane == 0) {
                     work[n & 1] = w;
                     mbar_arrive(&w_full[n & 1]);
@@ -391,7 +448,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     for (int t = 0; t < tiles; ++t)
                         for (int c = 0; c < G::kPanels; ++c)
                             tma_load_3d(sq + t * G::kTileBytes + c * G::kPanelBytes, &p.q_map, 64 * c, w.hk * group,
-                                   w.t0 + t * p.tile_tokens, q_full);
+                                        w.t0 + t * p.tile_tokens, q_full);
                 }
                 __syncwarp();
                 // lane x of the first `boxes` finds the page of its box of the block, one block ahead
@@ -543,13 +600,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                             int lo, hi;
                             key_range(w, i, lo, hi);
                             const int j0 = key_block(w, i);
-                            for (int r = lane; r < kKeys; r += 32)
+                            // (eight lanes a row of 128 bytes: no bank conflicts)
+                            for (int r = lane >> 3; r < kKeys; r += 4)
                                 if (j0 + r < lo || j0 + r >= hi)
-                                    for (int c = 0; c < G::kPanels; ++c)
 #pragma unroll
-                                        for (int x = 0; x < 8; ++x)
-                                            *reinterpret_cast<uint4*>(ring + at.slot * G::kTileBytes + c * G::kPanelBytes + r * 128 + 16 * x) =
-                                                make_uint4(0u, 0u, 0u, 0u);
+                                    for (int c = 0; c < G::kPanels; ++c)
+                                        *reinterpret_cast<uint4*>(ring + at.slot * G::kTileBytes + c * G::kPanelBytes + r * 128 + 16 * (lane & 7)) =
+                                            make_uint4(0u, 0u, 0u, 0u);
                             fence_proxy_async_smem();
                         }
                         __syncwarp();
@@ -577,13 +634,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         bool ok = true;
         for (int n = 0; ok; ++n) {
             if (!(ok = warp_wait(&w_full[n & 1], (n >> 1) & 1, kv.err, kErrTimeoutMma))) break;
-            const TcWork w = work[n & 1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&w_empty[n & 1]);
+            // (the entry is read where it is needed: registers are short here)
+            const TcWork& w = work[n & 1];
             if (w.tokens == 0) break;
             const int tiles = w.tokens > p.tile_tokens ? 2 : 1;
             if (t >= tiles) {  // no rows for this warpgroup
-                if (w.nb > 0 && lane == 0) mbar_arrive(&o_empty[t]);
+                const bool some = w.nb > 0;
+                __syncwarp();
+                if (lane == 0) {
+                    if (some) mbar_arrive(&o_empty[t]);
+                    mbar_arrive(&w_empty[n & 1]);
+                }
                 continue;
             }
             const bool live = in_tile < p.tile_tokens && tok < w.tokens;
@@ -599,7 +660,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             const int wlo = pos >= window ? pos - window + 1 : 0;  // first key of this row's window
             float m = -INFINITY, l = 0.0f;
             float s[kKeys];
-            for (int i = 0; i < w.nb; ++i) {
+            const int nb = w.nb;
+            for (int i = 0; i < nb; ++i) {
                 if (!(ok = warp_wait(&s_full[t], blocks & 1, kv.err, kErrTimeoutMma))) break;
                 tc_after();
 #pragma unroll
@@ -676,30 +738,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             }
             if (!ok) break;
             // ---- output
-            if (w.nb > 0) {
+            if (nb > 0) {
                 if (!(ok = warp_wait(&o_full[t], (blocks - 1) & 1, kv.err, kErrTimeoutMma))) break;
                 tc_after();
-#pragma unroll
-                for (int c = 0; c < DIM / 32; ++c) ld32(oa + 32 * c, s + 32 * c);
-                wait_ld();
-                tc_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&o_empty[t]);
             }
-            if (live) {
-                const int64_t row = int64_t(w.t0 + tok) * p.a.n_q_heads + w.hk * group + head;
-                const float inv = 1.0f / l;
-                const float lse2 = l > 0.0f ? m + log2f(l) : -INFINITY;
-                const int64_t part = int64_t(w.split) * p.a.n_tokens * p.a.n_q_heads + row;
-                if (p.part_o) p.part_lse[part] = lse2;
-                else if (p.a.lse) p.a.lse[row] = lse2 * 0.6931471805599453f;
-    #pragma unroll
-                for (int x = 0; x < DIM; ++x) s[x] = l > 0.0f ? s[x] * inv : 0.0f;  // (l is 0 where there was no block)
-                if (p.part_o) store_f32<DIM>(p.part_o + part * DIM, reinterpret_cast<float(&)[DIM]>(s));
-                else if (p.a.out_f32) store_f32<DIM>(static_cast<float*>(p.a.out) + row * DIM, reinterpret_cast<float(&)[DIM]>(s));
-                else store_f32<DIM>(static_cast<T*>(p.a.out) + row * DIM, reinterpret_cast<float(&)[DIM]>(s));
+            // a row whose keys were all here goes to the output, others to their part;
+            // an empty part has nothing to say but its log
+            const int split = w.split;
+            const bool to_part = p.part_o && (p.prefix || p.tails || w.parts > 1);
+            const int64_t row = int64_t(w.t0 + tok) * p.a.n_q_heads + w.hk * group + head;
+            const int64_t part = int64_t(split) * p.a.n_tokens * p.a.n_q_heads + row;
+            const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            if (live && p.part_o) p.part_lse[part] = to_part || split > 0 ? lse2 : kWritten;
+            if (split == 0 || nb > 0) {
+                if (live && !to_part && p.a.lse) p.a.lse[row] = lse2 * 0.6931471805599453f;
+                uint8_t* stage = outs + warp * 4096;
+                if (to_part) write_rows<DIM>(p.part_o, part * DIM, live, oa, nb > 0, inv, stage, lane, &o_empty[t]);
+                else if (p.a.out_f32) write_rows<DIM>(static_cast<float*>(p.a.out), row * DIM, live, oa, nb > 0, inv, stage, lane, &o_empty[t]);
+                else write_rows<DIM>(static_cast<T*>(p.a.out), row * DIM, live, oa, nb > 0, inv, stage, lane, &o_empty[t]);
             }
             __syncwarp();
+            if (lane == 0) mbar_arrive(&w_empty[n & 1]);
         }
     }
     tc_before();
@@ -727,6 +787,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     if (row >= rows) return;
     if (seq_of_token(p.a.kv, int(row / p.a.n_q_heads)) < 0) return;
     const float mine = lane < p.parts ? p.part_lse[lane * rows + row] : -INFINITY;
+    if (__shfl_sync(0xffffffffu, mine, 0) == kWritten) return;
     float M = mine;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -737,6 +798,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     float acc[V] = {};
     for (int i = 0; i < p.parts; ++i) {
         const float c = __shfl_sync(0xffffffffu, wt, i);
+        if (c == 0.0f) continue;  // (an empty part's o is not written)
         const float* src = p.part_o + (i * rows + row) * DIM + V * lane;
         if constexpr (V == 4) {
             const float4 v = *reinterpret_cast<const float4*>(src);
@@ -746,10 +808,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
             acc[0] += c * v.x, acc[1] += c * v.y;
         }
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
     for (int x = 0; x < V; ++x) acc[x] *= inv;
-    if (p.a.lse && lane == 0) p.a.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    if (p.a.lse && lane == 0) p.a.lse[row] = L != 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
     if (p.a.out_f32) {
         float* dst = static_cast<float*>(p.a.out) + row * DIM + V * lane;
         if constexpr (V == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -810,6 +872,7 @@ cudaError_t launch_tc(const AttnParams& a, bool prefix, int splits, float* part_
     memset(&p, 0, sizeof(p));
     p.a = a;
     p.prefix = prefix ? 1 : 0;
+    p.tails = !prefix && a.shared_len > 0 ? 1 : 0;
     p.splits = splits;
     p.part_o = part_o;
     p.part_lse = part_lse;
@@ -839,7 +902,7 @@ bool encode_cache_maps(bool f16, const KvView& kv, int keys, CUtensorMap* k, CUt
 // Tile pairs at most: each sequence may end with one that is not full.
 int64_t tc_pairs(int64_t n_tokens, int group, int n_seqs, bool prefix) {
     const int pair = 2 * (kTileRows / group);
-    return prefix ? (n_tokens + pair - 1) / pair : n_tokens / pair + (n_seqs < n_tokens ? n_seqs : n_tokens);
+    return prefix || n_seqs == 1 ? (n_tokens + pair - 1) / pair : n_tokens / pair + (n_seqs < n_tokens ? n_seqs : n_tokens);
 }
 
 cudaError_t launch_attn_tc(int dtype, const AttnParams& a, bool prefix, int splits, float* part_o, float* part_lse,
