@@ -179,6 +179,12 @@ __device__ __forceinline__ void write_rows(T* dst, int64_t at, bool live, uint32
                                            uint64_t* left) {
     constexpr int E = 128 / int(sizeof(T));  // elements a pass
     if (!live) at = -1;
+    T* to[8];  // of rows 4 k + lane / 8, this lane's 16 bytes
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int64_t a = __shfl_sync(0xffffffffu, at, 4 * k + (lane >> 3));
+        to[k] = a < 0 ? nullptr : dst + a + (lane & 7) * (E / 8);
+    }
 #pragma unroll
     for (int x0 = 0; x0 < DIM; x0 += E) {
         float v[E];
@@ -206,13 +212,15 @@ __device__ __forceinline__ void write_rows(T* dst, int64_t at, bool live, uint32
             *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
         }
         __syncwarp();
+        uint4 w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int r = 4 * k + (lane >> 3), c = lane & 7;
-            const int64_t to = __shfl_sync(0xffffffffu, at, r);
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
-            if (to >= 0) *reinterpret_cast<uint4*>(dst + to + x0 + c * (E / 8)) = w;
+            w[k] = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (to[k]) *reinterpret_cast<uint4*>(to[k] + x0) = w[k];
     }
 }
 
