@@ -128,7 +128,12 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_row_kernel(const __grid_c
 constexpr int kUnit = 64;                // keys of a unit
 constexpr uint64_t kSplitWaitNs = 2000000000ull;
 constexpr int kSplitWarps = 4;
-constexpr int kSplitThreads = 32 * (kSplitWarps + 1);  // the last warp is the producer
+// A second warpgroup for the producer (its other three warps only give up
+// registers): 128 registers a thread at launch, of which the consumers, who hold
+// a tile's queries and output, take most.
+constexpr int kSplitThreads = 2 * 32 * kSplitWarps;
+constexpr int kConsumerRegs = 176, kProducerRegs = 80;
+static_assert(kConsumerRegs + kProducerRegs <= 2 * 128, "registers the CTA was launched with");
 constexpr int kRows = 16;                // rows of a tile
 constexpr int kRingBytes = 96 * 1024;    // of one CTA; two CTAs fit on an SM
 
@@ -191,6 +196,16 @@ struct SeqWork {
 constexpr int kMostKeys = INT32_MAX - 4 * kUnit;  // of a sequence: key numbers stay in 32 bits
 __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, int group, bool report) {
     SeqWork w;
+    if (b == p.kv.n_seqs) {  // every token against the shared prefix (their positions are looked up)
+        const int total = p.kv.q_start[b];
+        const int64_t room = p.kv.table_stride << p.kv.page_shift, most = room < kMostKeys ? room : kMostKeys;
+        w.t0 = w.pos0 = w.lo = w.sinks = w.sink_units = 0;
+        w.tokens = total < p.n_tokens ? total : p.n_tokens;
+        w.end = int(p.shared_len < most ? p.shared_len : most);
+        w.units = (w.end + kUnit - 1) / kUnit;
+        w.row_tiles = (w.tokens * group + kRows - 1) / kRows;
+        return w;
+    }
     w.t0 = p.kv.q_start[b];
     w.tokens = p.kv.q_start[b + 1] - w.t0;
     const int kv = p.kv.kv_len[b];
@@ -220,14 +235,14 @@ struct Cursor {
     int b, rt, hk;
     SeqWork w;
 };
-__device__ __forceinline__ void next_tile(const AttnParams& p, Cursor& c, int group) {
+__device__ __forceinline__ void next_tile(const AttnParams& p, Cursor& c, int group, int seqs) {
     c.begin += c.w.units;
     if (++c.hk < p.kv.n_heads) return;
     c.hk = 0;
     if (++c.rt < c.w.row_tiles) return;
     c.rt = 0;
     do {
-        if (++c.b >= p.kv.n_seqs) return;
+        if (++c.b >= seqs) return;
         c.w = seq_work(p, c.b, group, false);
     } while (c.w.row_tiles == 0);
 }
@@ -244,12 +259,12 @@ __device__ __forceinline__ int unit_keys(const SeqWork& w, int u, int& lo, int& 
 // rows; and the workers that share the tile.
 struct UnitInfo {
     int j0, lo, hi;
-    int flags;           // kSink, kOpens, kCloses (for this worker)
+    int flags;           // kSink, kOpens, kCloses (for this worker), kPrefix
     int t0, r0, rows;    // the sequence's first token, the tile's first row and the rows from it on
     int hk, pos0;
     int wf, parts, part; // first worker, workers after it, and the part of the scratch that the first one writes
 };
-constexpr int kSink = 1, kOpens = 2, kCloses = 4;
+constexpr int kSink = 1, kOpens = 2, kCloses = 4, kPrefix = 8;
 
 struct SplitParams {
     CUtensorMap k_map;  // [pages][heads][slots][dim], boxes of min(page, 64) keys x 64
@@ -258,6 +273,7 @@ struct SplitParams {
     float* part_o;    // not null: the rows are a part to be joined (o / l, base-2 log of the sum)
     float* part_lse;
     int beside;       // 1: launched beside the kernel before it, which belongs to the same call
+    int prefix;       // 1: the shared prefix, too: its tiles end the line, and give part 0, the tails part 1
 };
 
 // Quotients of non-negative numbers, in 32 bits where they fit (nearly always).
@@ -266,6 +282,95 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
     return a / b;
 }
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSplitWarps) : "memory"); }
+
+// Four elements of row r of a tile (its sum o, not divided yet).
+template <typename T, int DIM>
+__device__ __forceinline__ void write_four(const SplitParams& pp, const UnitInfo& tile, int r, int d, float M, float L, float4 v) {
+    const AttnParams& p = pp.a;
+    const int group = p.n_q_heads / p.kv.n_heads, rr = tile.r0 + r;
+    const int64_t row = int64_t(tile.t0 + rr / group) * p.n_q_heads + tile.hk * group + rr % group;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+    if (pp.part_o) {
+        const int64_t at = row + (pp.prefix && !(tile.flags & kPrefix) ? int64_t(p.n_tokens) * p.n_q_heads : 0);
+        *reinterpret_cast<float4*>(pp.part_o + at * DIM + d) = v;
+        if (d == 0) pp.part_lse[at] = L == 0.0f ? -INFINITY : M + log2f(L);
+        return;
+    }
+    if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * DIM + d) = v;
+    else *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * DIM + d) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+    if (p.lse && d == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// The parts of a tile that several workers shared, joined by the consumers of
+// the last of them to arrive.
+template <typename T, int DIM>
+__device__ __forceinline__ void join_parts(const SplitParams& pp, const UnitInfo& tile, float* buf) {
+    float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(pp.a.scratch) + kCounterBytes);
+    float* buf_ml = buf + kSplitWarps * 8 * DIM;
+    const int live = tile.rows < kRows ? tile.rows : kRows, parts = tile.parts + 1;
+    const float* const begin = partials + int64_t(tile.part) * partial_floats<DIM>();
+    const float* const rest = partials + int64_t(2 * (tile.wf + 1)) * partial_floats<DIM>();
+    constexpr int64_t kStep = 2 * partial_floats<DIM>();
+    const auto src = [&](int i) -> const float* { return i == 0 ? begin : rest + (i - 1) * kStep; };
+    // eight threads a row find its maximum and sum, and leave each part's
+    // weight in the buffer
+    float* weight = buf;  // [16][parts], where that fits
+    const bool fits = kRows * parts <= kSplitWarps * 8 * DIM;
+    const int r8 = threadIdx.x >> 3, i8 = threadIdx.x & 7;
+    float M = -INFINITY, L = 0.0f;
+    if (r8 < live) {
+#pragma unroll 4
+        for (int i = i8; i < parts; i += 8) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(src(i) + kRows * DIM + 2 * r8));
+            const float mn = fmaxf(M, ml.x);
+            if (mn != -INFINITY) L = L * exp2_approx(M - mn) + ml.y * exp2_approx(ml.x - mn);
+            M = mn;
+            if (fits) weight[r8 * parts + i] = ml.x;
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, M, o), ol = __shfl_xor_sync(0xffffffffu, L, o);
+        const float mn = fmaxf(M, om);
+        if (mn != -INFINITY) L = L * exp2_approx(M - mn) + ol * exp2_approx(om - mn);
+        M = mn;
+    }
+    if (r8 < live) {
+        if (fits)
+            for (int i = i8; i < parts; i += 8) {
+                const float m = weight[r8 * parts + i];
+                weight[r8 * parts + i] = m == -INFINITY ? 0.0f : exp2_approx(m - M);
+            }
+        if (i8 == 0) *reinterpret_cast<float2*>(buf_ml + 2 * r8) = make_float2(M, L);
+    }
+    consumers_sync();
+    for (int x = threadIdx.x; x < live * (DIM / 4); x += 32 * kSplitWarps) {
+        const int r = x / (DIM / 4), d = x % (DIM / 4) * 4;
+        const float2 ml = *reinterpret_cast<const float2*>(buf_ml + 2 * r);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        // eight parts' loads in flight at a time
+        for (int w0 = 0; w0 < parts; w0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+                v[y] = __ldcg(reinterpret_cast<const float4*>(src(w0 + y < parts ? w0 + y : parts - 1) + r * DIM + d));
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                if (w0 + y >= parts) break;
+                float c;
+                if (fits) {
+                    c = weight[r * parts + w0 + y];
+                } else {
+                    const float m = __ldcg(src(w0 + y) + kRows * DIM + 2 * r);
+                    c = m == -INFINITY ? 0.0f : exp2_approx(m - ml.x);
+                }
+                acc.x += c * v[y].x, acc.y += c * v[y].y, acc.z += c * v[y].z, acc.w += c * v[y].w;
+            }
+        }
+        write_four<T, DIM>(pp, tile, r, d, ml.x, ml.y, acc);
+    }
+}
 
 template <typename T, int DIM>
 __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __grid_constant__ SplitParams pp) {
@@ -278,11 +383,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     float* buf_ml = buf + kSplitWarps * 8 * DIM;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes + G::kJoin);
     uint64_t* empty = full + NS;
-    int64_t* scan = reinterpret_cast<int64_t*>(empty + NS);  // [5]
-    Cursor* start = reinterpret_cast<Cursor*>(scan + kSplitWarps + 1);
+    int64_t* scan = reinterpret_cast<int64_t*>(empty + NS);  // [8]
+    Cursor* start = reinterpret_cast<Cursor*>(scan + 2 * kSplitWarps);
     UnitInfo* info = reinterpret_cast<UnitInfo*>(start + 1);  // [NS], and the first unit's
     int* last_flag = reinterpret_cast<int*>(info + NS + 1);
-    static_assert((2 * NS + kSplitWarps + 1) * 8 + sizeof(Cursor) + (NS + 1) * sizeof(UnitInfo) + 4 <= G::kMisc,
+    static_assert((2 * NS + 2 * kSplitWarps) * 8 + sizeof(Cursor) + (NS + 1) * sizeof(UnitInfo) + 4 <= G::kMisc,
                   "barriers, units and the worker's place");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -300,12 +405,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     if (!pp.beside) pdl_wait_prior_grid();
     pdl_launch_dependents();
     const int group = p.n_q_heads / p.kv.n_heads;
-    const int B = p.kv.n_seqs;
+    const int B = p.kv.n_seqs + pp.prefix;
 
     // ---- the line's length, and where this worker's share begins
     int64_t mine = 0;
     const int per = (B + kSplitThreads - 1) / kSplitThreads, b0 = threadIdx.x * per;
-    SeqWork own;  // of the thread's last sequence (its only one, for up to 160 sequences)
+    SeqWork own;  // of the thread's last sequence (its only one, for up to 256 sequences)
     for (int b = b0; b < b0 + per && b < B; ++b) {
         own = seq_work(p, b, group, blockIdx.x == 0);
         mine += int64_t(own.row_tiles) * p.kv.n_heads * own.units;
@@ -320,11 +425,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     __syncthreads();
     int64_t U = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w <= kSplitWarps; ++w) {
+    for (int w = 0; w < 2 * kSplitWarps; ++w) {
         if (w < warp) before += scan[w];
         U += scan[w];
     }
-    const int64_t N = gridDim.x < U ? gridDim.x : U;
+    // (two units each at least: one token over 1023 keys took 8.5 us with one)
+    const int64_t pairs = (U + 1) / 2, N = gridDim.x < pairs ? gridDim.x : pairs;
     if (blockIdx.x >= N) {
         if (pp.beside) pdl_wait_prior_grid();
         return;
@@ -358,7 +464,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     const auto describe = [&](const Cursor& c, int u, UnitInfo& x) {
         x.j0 = unit_keys(c.w, u, x.lo, x.hi);
         const int64_t begin = c.begin, end = c.begin + c.w.units, here = begin + u;
-        x.flags = (u < c.w.sink_units ? kSink : 0) | (here == first || u == 0 ? kOpens : 0) | (here + 1 == last || here + 1 == end ? kCloses : 0);
+        x.flags = (u < c.w.sink_units ? kSink : 0) | (here == first || u == 0 ? kOpens : 0) | (here + 1 == last || here + 1 == end ? kCloses : 0) |
+                  (c.b == p.kv.n_seqs ? kPrefix : 0);
         x.t0 = c.w.t0;
         x.r0 = kRows * c.rt;
         x.rows = c.w.tokens * group - x.r0;
@@ -374,7 +481,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     };
     if (threadIdx.x == 0) describe(*start, int(first - start->begin), info[NS]);
 
-    if (warp == kSplitWarps) {
+    if (warp >= kSplitWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        if (warp > kSplitWarps) {
+            if (pp.beside) pdl_wait_prior_grid();
+            return;
+        }
         // ---- producer: a lane for each page of a unit
         Cursor cur = *start;
         int ui = int(first - cur.begin);  // unit of the tile
@@ -385,7 +497,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         const auto page_for = [&](int u) -> int {
             int lo, hi;
             const int j = unit_keys(cur.w, u, lo, hi) + lane * page_keys;
-            return lane < boxes && j + page_keys > lo && j < hi ? page_of(p.kv, cur.b, j) : -1;
+            return lane < boxes && j + page_keys > lo && j < hi ? page_of(p.kv, cur.b < p.kv.n_seqs ? cur.b : 0, j) : -1;
         };
         int page = page_for(ui);
         int slot = 0;
@@ -400,7 +512,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
             describe(cur, ui, x);
             if (left > 1) {  // the next unit's pages are looked up while this one's room is awaited
                 if (++ui == cur.w.units) {
-                    next_tile(p, cur, group);
+                    next_tile(p, cur, group, B);
                     ui = 0;
                 }
                 page = page_for(ui);
@@ -442,6 +554,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     }
 
     // ---- consumers
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
     uint32_t qf[KS][4];
     float o[DIM / 8][4], m[2], l[2];
     int rpos[2];             // positions of this lane's two rows (-1: none)
@@ -449,15 +562,19 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     // A tile's rows: 16 rt + lane / 4 and eight further.
     const auto open_tile = [&](const UnitInfo& x) {
         const int live_rows = x.rows < kRows ? x.rows : kRows;
-        pos_first = x.pos0 + x.r0 / group;
-        pos_last = x.pos0 + (x.r0 + live_rows - 1) / group;
-        if (pos_last < -1) pos_last = -1;
+        int low = INT32_MAX, high = -1;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = (lane >> 2) + 8 * i;
             const bool live = r < live_rows;
             const int tok = (x.r0 + (live ? r : 0)) / group, g = x.r0 + (live ? r : 0) - tok * group;
-            rpos[i] = live && x.pos0 + tok >= 0 ? x.pos0 + tok : -1;
+            int pos = x.pos0 + tok;
+            if (x.flags & kPrefix) {
+                const int seq = live ? seq_of_token(p.kv, tok) : -1;
+                pos = seq < 0 ? -1 : int(position_of(p.kv, seq, tok));
+            }
+            rpos[i] = live && pos >= 0 ? pos : -1;
+            if (live) low = low < rpos[i] ? low : rpos[i], high = high > rpos[i] ? high : rpos[i];
             const T* q = static_cast<const T*>(p.q) + int64_t(x.t0 + tok) * p.q_stride + int64_t(x.hk * group + g) * DIM + 2 * (lane & 3);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
@@ -465,6 +582,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                 qf[k][i + 2] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
             }
         }
+        pos_first = __reduce_min_sync(0xffffffffu, low);
+        pos_last = __reduce_max_sync(0xffffffffu, high);
     };
     consumers_sync();  // the first unit's description
     open_tile(info[NS]);
@@ -600,20 +719,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         if (left > 1) open_tile(info[slot]);
         const int rows = done.rows;  // (16 at most count)
         const auto part_at = [&](int i) -> float* { return partials + int64_t(i) * partial_floats<DIM>(); };
-        const auto finish = [&](int r, int d, float M, float L, float4 v) {
-            const int rr = done.r0 + r;
-            const int64_t row = int64_t(done.t0 + rr / group) * p.n_q_heads + done.hk * group + rr % group;
-            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-            if (pp.part_o) {
-                *reinterpret_cast<float4*>(pp.part_o + row * DIM + d) = v;
-                if (d == 0) pp.part_lse[row] = L == 0.0f ? -INFINITY : M + log2f(L);
-                return;
-            }
-            if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * DIM + d) = v;
-            else *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * DIM + d) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
-            if (p.lse && d == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-        };
+        const auto finish = [&](int r, int d, float M, float L, float4 v) { write_four<T, DIM>(pp, done, r, d, M, L, v); };
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (8 * i >= rows) break;
@@ -669,42 +775,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                 }
             }
             consumers_sync();
-            if (*last_flag) {
-                const int live = rows < kRows ? rows : kRows, parts = done.parts;  // beyond the first
-                const float *begin = part_at(done.part), *rest = part_at(2 * (done.wf + 1));
-                constexpr int64_t kStep = 2 * partial_floats<DIM>();
-                for (int x = threadIdx.x; x < live * (DIM / 4); x += 32 * kSplitWarps) {
-                    const int r = x / (DIM / 4), d = x % (DIM / 4) * 4;
-                    const int at_ml = kRows * DIM + 2 * r, at_o = r * DIM + d;
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(begin + at_ml));
-                    float M = ml.x, L = ml.y;
-                    float4 acc = __ldcg(reinterpret_cast<const float4*>(begin + at_o));
-                    // eight parts' loads in flight at a time
-                    for (int w0 = 0; w0 < parts; w0 += 8) {
-                        float2 e[8];
-                        float4 v[8];
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const float* f = rest + (w0 + y < parts ? w0 + y : parts - 1) * kStep;
-                            e[y] = __ldcg(reinterpret_cast<const float2*>(f + at_ml));
-                            v[y] = __ldcg(reinterpret_cast<const float4*>(f + at_o));
-                        }
-                        float mn = M;
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) mn = fmaxf(mn, e[y].x);
-                        const float a = M == -INFINITY ? 0.0f : exp2_approx(M - mn);
-                        M = mn;
-                        L *= a, acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const float c = w0 + y < parts && e[y].x != -INFINITY ? exp2_approx(e[y].x - mn) : 0.0f;
-                            L += c * e[y].y;
-                            acc.x += c * v[y].x, acc.y += c * v[y].y, acc.z += c * v[y].z, acc.w += c * v[y].w;
-                        }
-                    }
-                    finish(r, d, M, L, acc);
-                }
-            }
+            if (*last_flag) join_parts<T, DIM>(pp, done, buf);
         }
         consumers_sync();  // the buffer is read
     }
@@ -728,13 +799,14 @@ cudaError_t launch_split(SplitParams& p, int sm_count, cudaStream_t s) {
     return launch_serial(attn_split_kernel<T, DIM>, dim3(unsigned(workers)), kSplitThreads, SplitGeom<DIM>::kSmem, s, p);
 }
 
-cudaError_t launch_split_any(int dtype, const AttnParams& a, float* part_o, float* part_lse, bool beside, int sm_count,
-                             cudaStream_t s) {
+cudaError_t launch_split_any(int dtype, const AttnParams& a, float* part_o, float* part_lse, bool beside, bool prefix,
+                             int sm_count, cudaStream_t s) {
     SplitParams p;
     p.a = a;
     p.part_o = part_o;
     p.part_lse = part_lse;
     p.beside = beside ? 1 : 0;
+    p.prefix = prefix ? 1 : 0;
     const bool f16 = dtype == QX_F16;
     if (a.kv.head_dim == 128)
         return f16 ? launch_split<__half, 128>(p, sm_count, s) : launch_split<__nv_bfloat16, 128>(p, sm_count, s);
@@ -751,6 +823,7 @@ constexpr size_t kSplitScratch = kCounterBytes + size_t(kMaxWorkers) * 2 * parti
 // split kMaxSplits ways, but no more than kPartRows rows in all (calls of that
 // many rows fill the GPU without splitting their keys), or two parts of a call
 // whose shared prefix is taken apart.
+constexpr int kPrefixUnits = 10, kShortPrefix = 4096;
 constexpr int kMaxSplits = 31;  // of one launch: with the tails' part a row has at most 32
 constexpr int64_t kPartRows = 196608, kMaxSharedRows = 131072;
 int64_t part_rows(int64_t rows) {
@@ -806,6 +879,17 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
     cudaError_t e;
     const int64_t spare = part_rows(rows);
     if (p.shared_len > 0) {
+        // A short prefix for few rows: the split kernel takes it with the
+        // tails, though it reads it once for every 16 rows.  (16 sequences
+        // behind 2000 keys: 23 us, against 32 with a launch of its own; 64
+        // behind 2000 or 16 behind 8000: 49 and 41 against 46 and 37; 4 behind
+        // 8000, whose tiles many workers share: 36 against 28.)
+        const int64_t units = (int64_t(p.n_tokens) * group + kRows - 1) / kRows * p.kv.n_heads * ((p.shared_len + kUnit - 1) / kUnit);
+        if (!many && p.shared_len <= kShortPrefix && units <= int64_t(kPrefixUnits) * 2 * sm_count) {
+            j.parts = 2;
+            e = launch_split_any(dtype, p, part_o, part_lse, false, true, sm_count, s);
+            return e != cudaSuccess ? e : launch_attn_join(dtype, j, s);
+        }
         // the prefix, the tails beside it, and both joined
         j.parts = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, true) * p.kv.n_heads, (p.shared_len + 127) / 128, rows, spare - rows,
                              sm_count);
@@ -813,10 +897,10 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
         float* o = part_o + j.parts * rows * dim;
         float* l = part_lse + j.parts * rows;
         ++j.parts;
-        e = many ? launch_attn_tc(dtype, p, false, 1, o, l, counter, sm_count, s) : launch_split_any(dtype, p, o, l, true, sm_count, s);
+        e = many ? launch_attn_tc(dtype, p, false, 1, o, l, counter, sm_count, s) : launch_split_any(dtype, p, o, l, true, false, sm_count, s);
         return e != cudaSuccess ? e : launch_attn_join(dtype, j, s);
     }
-    if (!many) return launch_split_any(dtype, p, nullptr, nullptr, false, sm_count, s);
+    if (!many) return launch_split_any(dtype, p, nullptr, nullptr, false, false, sm_count, s);
     int64_t keys = p.kv.table_stride << p.kv.page_shift;
     if (p.window > 0 && p.window + 256 < keys) keys = p.window + 256;
     const int n = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, false) * p.kv.n_heads, (keys + 127) / 128, rows, spare, sm_count);
