@@ -29,12 +29,6 @@ def rotate(x, c, s, interleaved):
     return x
 
 
-def visible(pos, window, sinks):
-    """The keys that a token at `pos` sees."""
-    j = np.arange(max(0, pos + 1))
-    return j if window == 0 else j[(j > pos - window) | (j < sinks)]
-
-
 def attention(q, keys, values, positions, scale, window=0, sinks=0):
     """q [tokens, hq, d] against the sequence's keys and values [kv, hk, d] (64 bits).
 
@@ -43,18 +37,22 @@ def attention(q, keys, values, positions, scale, window=0, sinks=0):
     g = hq // keys.shape[1] if keys.shape[1] else 1
     out, mass = np.zeros((T, hq, d)), np.zeros((T, hq, d))
     lse, top = np.full((T, hq), -np.inf), np.zeros((T, hq))
-    for t, pos in enumerate(positions):
-        j = visible(pos, window, sinks)
-        if len(j) == 0:
-            continue
-        k, v = keys[j].repeat(g, axis=1), values[j].repeat(g, axis=1)  # [n, hq, d]
-        s = np.einsum("hd,nhd->hn", q[t], k) * scale
+    positions, j = np.asarray(positions)[:, None], np.arange(len(keys))[None]
+    see = j <= positions
+    if window:
+        see &= (j > positions - window) | (j < sinks)
+    rows = see.any(1)
+    if not rows.any():
+        return out, lse, mass, top
+    see = see[rows]
+    for h in range(hq):
+        k, v = keys[:, h // g], values[:, h // g]
+        s = np.where(see, (q[rows, h] @ k.T) * scale, -np.inf)
         m = s.max(1, keepdims=True)
         p = np.exp(s - m)
         l = p.sum(1, keepdims=True)
-        out[t] = np.einsum("hn,nhd->hd", p / l, v)
-        mass[t] = np.einsum("hn,nhd->hd", p / l, np.abs(v))
-        lse[t], top[t] = (m + np.log(l))[:, 0], np.abs(s).max(1)
+        out[rows, h], mass[rows, h] = (p / l) @ v, (p / l) @ np.abs(v)
+        lse[rows, h], top[rows, h] = (m + np.log(l))[:, 0], np.where(see, np.abs(s), 0).max(1)
     return out, lse, mass, top
 
 
