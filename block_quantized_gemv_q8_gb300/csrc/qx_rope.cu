@@ -24,34 +24,33 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     const int head = item / per_head, c = item - head * per_head;
     const int hkv = p.kv.n_heads;
     if (head >= p.n_q_heads + 2 * hkv) return;
-    const int seq = seq_of_token(p.kv, t);
-    if (seq < 0) return;
-    const int64_t pos = position_of(p.kv, seq, t);
     const int dim = p.kv.head_dim;
-    const S* src;
-    D* dst;
-    if (head < p.n_q_heads) {
-        src = static_cast<const S*>(p.q) + t * p.q_stride + int64_t(head) * dim;
-        dst = static_cast<D*>(p.q_out) + (int64_t(t) * p.n_q_heads + head) * dim;
-    } else {
-        const bool is_v = head >= p.n_q_heads + hkv;
-        const int h = head - p.n_q_heads - (is_v ? hkv : 0);
-        src = static_cast<const S*>(is_v ? p.v : p.k) + t * (is_v ? p.v_stride : p.k_stride) + int64_t(h) * dim;
-        if (pos < 0) return;
-        const int page = page_of(p.kv, seq, pos);
-        if (page < 0) return;
-        dst = reinterpret_cast<D*>(is_v ? p.kv.v : p.kv.k) + slot_offset(p.kv, page, h, pos);
-    }
-    const bool turns = head < p.n_q_heads + hkv && c * 8 < p.rot;
-    float v[8];
+    const bool is_q = head < p.n_q_heads, is_v = head >= p.n_q_heads + hkv;
+    const int h = is_q ? head : head - p.n_q_heads - (is_v ? hkv : 0);
+    const S* src = (is_q   ? static_cast<const S*>(p.q) + t * p.q_stride
+                    : is_v ? static_cast<const S*>(p.v) + t * p.v_stride
+                           : static_cast<const S*>(p.k) + t * p.k_stride) + int64_t(h) * dim;
+    const bool turns = !is_v && c * 8 < p.rot;
     // Half-split pairs: elements 4 c .. 4 c + 3 and their partners half a
     // rotation on; otherwise elements 8 c .. 8 c + 7.
     const bool split = turns && !p.interleaved;
     const int half = p.rot / 2;
     const int e0 = split ? 4 * c : 8 * c, e1 = split ? 4 * c + half : 8 * c + 4;
-    float lo[4], hi[4];
-    load_f32<4>(src + e0, lo);
+    float lo[4], hi[4], v[8];
+    load_f32<4>(src + e0, lo);  // on their way while the token's place is looked up
     load_f32<4>(src + e1, hi);
+    const int seq = seq_of_token(p.kv, t);
+    if (seq < 0) return;
+    const int64_t pos = position_of(p.kv, seq, t);
+    D* dst;
+    if (is_q) {
+        dst = static_cast<D*>(p.q_out) + (int64_t(t) * p.n_q_heads + head) * dim;
+    } else {
+        if (pos < 0) return;
+        const int page = page_of(p.kv, seq, pos);
+        if (page < 0) return;
+        dst = reinterpret_cast<D*>(is_v ? p.kv.v : p.kv.k) + slot_offset(p.kv, page, h, pos);
+    }
     if (pos < 0) {  // padding: a query row of zeros
 #pragma unroll
         for (int i = 0; i < 4; ++i) lo[i] = hi[i] = 0.0f;
