@@ -824,8 +824,8 @@ constexpr size_t kSplitScratch = kCounterBytes + size_t(kMaxWorkers) * 2 * parti
 // many rows fill the GPU without splitting their keys), or two parts of a call
 // whose shared prefix is taken apart.
 constexpr int kPrefixUnits = 10, kShortPrefix = 4096;
-constexpr int kMaxSplits = 31;  // of one launch: with the tails' part a row has at most 32
-constexpr int64_t kPartRows = 196608, kMaxSharedRows = 131072;
+constexpr int kMaxSplits = 31;  // parts of one launch: with the tails' part a row has at most 32
+constexpr int64_t kPartRows = 262144, kMaxSharedRows = 131072;
 int64_t part_rows(int64_t rows) {
     int64_t n = rows < kPartRows / kMaxSplits ? rows * kMaxSplits : kPartRows;
     const int64_t two = 2 * (rows < kMaxSharedRows ? rows : kMaxSharedRows);
@@ -833,17 +833,17 @@ int64_t part_rows(int64_t rows) {
     return (n + 63) / 64 * 64;  // 256-byte multiples
 }
 
-// CTAs that share a tile pair's keys: as many as give every SM one, where the
-// pairs alone do not.  (More parts than SMs cost more than their better balance
-// gains, since each is written and read in f32: a chunk of 512 tokens over
-// 16384 keys, 64 pairs, took 115 us with 2 parts each and 122 with 7; 4096
-// causal tokens, 512 pairs, 107 us with one and 164 with two.)
-int splits_for(int64_t pairs, int64_t blocks, int64_t rows, int64_t spare_rows, int sm_count) {
-    int64_t n = sm_count / (pairs > 0 ? pairs : 1);
-    if (n > kMaxSplits) n = kMaxSplits;
-    if (n > blocks) n = blocks;
+// Parts of a row at most where the tensor-core kernel shares the key blocks of
+// all pairs out evenly, or 0: every pair in one CTA.  Even shares are for calls
+// of few pairs (fewer than kEvenPairs an SM, times the key heads): with more,
+// the counter balances them, and parts cost their f32 bytes and a launch.  The
+// scheduler of every CTA reads every sequence, so there are to be few of them.
+constexpr int kEvenPairs = 3, kEvenSeqs = 32;
+int slots_for(int64_t pairs, int64_t blocks, int seqs, int64_t rows, int64_t spare_rows, int sm_count) {
+    if (pairs >= int64_t(kEvenPairs) * sm_count || seqs > kEvenSeqs || blocks < 12) return 0;
+    int64_t n = blocks + 1 < kMaxSplits ? blocks + 1 : kMaxSplits;
     if (n * rows > spare_rows) n = spare_rows / rows;
-    return n < 1 ? 1 : int(n);
+    return n < 5 ? 0 : int(n);  // (with fewer the shares have to grow to fit a long pair's parts in)
 }
 
 }  // namespace
@@ -891,22 +891,23 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
             return e != cudaSuccess ? e : launch_attn_join(dtype, j, s);
         }
         // the prefix, the tails beside it, and both joined
-        j.parts = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, true) * p.kv.n_heads, (p.shared_len + 127) / 128, rows, spare - rows,
-                             sm_count);
-        if ((e = launch_attn_tc(dtype, p, true, j.parts, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
+        const int slots = slots_for(0, (p.shared_len + 127) / 128, 1, rows, spare - rows, sm_count);
+        if ((e = launch_attn_tc(dtype, p, true, slots, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
+        j.parts = slots > 0 ? slots : 1;
         float* o = part_o + j.parts * rows * dim;
         float* l = part_lse + j.parts * rows;
         ++j.parts;
-        e = many ? launch_attn_tc(dtype, p, false, 1, o, l, counter, sm_count, s) : launch_split_any(dtype, p, o, l, true, false, sm_count, s);
+        e = many ? launch_attn_tc(dtype, p, false, 0, o, l, counter, sm_count, s) : launch_split_any(dtype, p, o, l, true, false, sm_count, s);
         return e != cudaSuccess ? e : launch_attn_join(dtype, j, s);
     }
     if (!many) return launch_split_any(dtype, p, nullptr, nullptr, false, false, sm_count, s);
     int64_t keys = p.kv.table_stride << p.kv.page_shift;
-    if (p.window > 0 && p.window + 256 < keys) keys = p.window + 256;
-    const int n = splits_for(tc_pairs(p.n_tokens, group, p.kv.n_seqs, false) * p.kv.n_heads, (keys + 127) / 128, rows, spare, sm_count);
-    if (n == 1) return launch_attn_tc(dtype, p, false, 1, nullptr, nullptr, counter, sm_count, s);
-    if ((e = launch_attn_tc(dtype, p, false, n, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
-    j.parts = n;
+    if (p.window > 0 && p.window + p.sinks + 256 < keys) keys = p.window + p.sinks + 256;
+    const int64_t pairs = tc_pairs(p.n_tokens, group, p.kv.n_seqs, false) * p.kv.n_heads;
+    const int slots = slots_for(pairs, (keys + 127) / 128, p.kv.n_seqs, rows, spare, sm_count);
+    if (slots == 0) return launch_attn_tc(dtype, p, false, 0, nullptr, nullptr, counter, sm_count, s);
+    if ((e = launch_attn_tc(dtype, p, false, slots, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
+    j.parts = slots;
     return launch_attn_join(dtype, j, s);
 }
 

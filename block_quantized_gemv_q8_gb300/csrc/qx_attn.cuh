@@ -56,9 +56,10 @@ struct JoinParams {
 int64_t tc_pairs(int64_t n_tokens, int group, int n_seqs, bool prefix);
 // The tokens' attention on the tensor cores: over all their keys (from
 // shared_len on), or, `prefix`, over keys [0, shared_len) of the first
-// sequence.  part_o null: written to the output (one split).  counter: two
-// words of scratch, zero between calls.
-cudaError_t launch_attn_tc(int dtype, const AttnParams& a, bool prefix, int splits, float* part_o, float* part_lse,
+// sequence.  slots 0: every tile pair in one CTA; else (at least 3) the blocks
+// of keys shared out evenly, rows leaving up to `slots` parts.  part_o null:
+// written to the output.  counter: two words of scratch, zero between calls.
+cudaError_t launch_attn_tc(int dtype, const AttnParams& a, bool prefix, int slots, float* part_o, float* part_lse,
                            unsigned* counter, int sm_count, cudaStream_t s);
 cudaError_t launch_attn_join(int dtype, const JoinParams& p, cudaStream_t s);
 

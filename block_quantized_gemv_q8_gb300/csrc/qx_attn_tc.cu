@@ -21,10 +21,15 @@
 // against 128 x 128 exponentials: the tensor cores and the softmax warps take
 // about the same time, and which of them bounds depends on the head size.
 //
-// The CTAs are persistent (one an SM) and take tile pairs from a counter, those
-// with the most keys first.  A third warpgroup serves the two: a producer, which
-// takes the pairs and runs ahead with the copies, a warp that issues the MMAs, and a warp that zeroes values that no row sees.  The
-// next pair's first scores are computed during this pair's epilogue.
+// The CTAs are persistent, one an SM.  Where there are many pairs they take them
+// from a counter, those with the most keys first; where there are few (a short
+// chunk, a shared prefix, contexts of very different lengths) each takes an
+// equal share of the line of all pairs' blocks.  A pair whose keys several CTAs
+// share leaves parts (o / l and the base-2 log of its sum) that
+// attn_join_kernel joins.  A third warpgroup serves the two: a scheduler, a
+// producer that runs ahead with the copies, a warp that issues the MMAs, and one
+// that zeroes values that no row sees.  The next pair's first scores are
+// computed during this pair's epilogue.
 //
 // A row's keys may be split over several CTAs (few rows, long context); each
 // part then leaves o / l and the base-2 log of its sum, which
@@ -46,14 +51,15 @@ namespace {
 constexpr int kKeys = 128;             // keys of a block
 constexpr int kTileRows = 128;         // rows of a tile; two tiles a CTA
 constexpr int kSoftmaxWarps = 8;       // two warpgroups
-// A third warpgroup: the MMA issuer, the producer, the warp that zeroes, and one
-// that only gives up registers.  An SM partition holds three of the CTA's warps, so 168
+// A third warpgroup: the MMA issuer, the producer, the warp that zeroes, and the
+// scheduler.  An SM partition holds three of the CTA's warps, so 168
 // registers a thread at launch; the softmax warps hold a row of S each.
 constexpr int kTcThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "registers the CTA was launched with");
 constexpr float kRescale = 8.0f;
-constexpr int kMinPart = 8;            // blocks: a part costs some 5 us beside them
+constexpr int kFixed = 3;              // blocks that a pair's fixed cost (some 5 us) is worth
+constexpr int kMinPart = 8;            // blocks of a range at least: a part costs some 5 us beside them
 constexpr float kWritten = INFINITY;   // as a row's first base-2 log: the row is in the output already
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
@@ -73,11 +79,11 @@ struct TcAttnParams {
     CUtensorMap v_map;
     AttnParams a;
     int tile_tokens;    // tokens of a tile: 128 / group
-    int splits;         // CTAs that share a tile pair's keys
+    int slots;          // 0: pairs from a counter; else ranges of blocks, and a row's parts at most
     int prefix;         // 1: every token against keys [0, shared_len)
     int tails;          // 1: the parts of a call whose prefix is taken apart
-    float* part_o;      // parts: [splits][tokens * heads][dim], or null: write the output
-    float* part_lse;    // [splits][tokens * heads]
+    float* part_o;      // parts: [slots][tokens * heads][dim], or null: write the output
+    float* part_lse;    // [slots][tokens * heads]
     unsigned* counter;  // pairs taken beyond each CTA's first, and CTAs done; zero between calls
 };
 
@@ -230,7 +236,7 @@ __device__ __forceinline__ void write_rows(T* dst, int64_t at, bool live, uint32
 struct TcWork {
     int b, t0, tokens, pos0, lo, end, sinks, sink_blocks, blocks;
     int hk, split, i0, nb;  // key head, part, and its blocks [i0, i0 + nb)
-    int parts;              // parts that have blocks
+    int parts;              // parts of the pair's rows
 };
 __device__ __forceinline__ int key_block(const TcWork& w, int i) {  // first key of the i-th block
     return (i < w.sink_blocks ? i : w.lo / kKeys + (i - w.sink_blocks)) * kKeys;
@@ -240,35 +246,71 @@ __device__ __forceinline__ void key_range(const TcWork& w, int i, int& lo, int& 
     hi = i < w.sink_blocks ? w.sinks : w.end;
 }
 
+// Sequence b as the tensor cores' pairs of tiles see it: its first token, its
+// tokens (none where q_start is no ascending list of this call's tokens) and
+// its keys.  A prefix is one pseudo-sequence of all tokens.
+struct TcSeq {
+    int t0, tokens, len;
+};
+__device__ __forceinline__ TcSeq tc_seq(const TcAttnParams& p, int b) {
+    const KvView& kv = p.a.kv;
+    TcSeq q;
+    if (p.prefix) {
+        q.t0 = q.len = 0;
+        q.tokens = kv.q_start[kv.n_seqs] < p.a.n_tokens ? kv.q_start[kv.n_seqs] : p.a.n_tokens;
+        return q;
+    }
+    q.t0 = kv.q_start[b];
+    q.tokens = kv.q_start[b + 1] - q.t0;
+    q.len = kv.kv_len[b];
+    if (q.tokens < 0 || q.t0 < 0 || q.t0 + q.tokens > p.a.n_tokens) q.tokens = 0;
+    return q;
+}
+__device__ __forceinline__ int tc_seqs(const TcAttnParams& p) { return p.prefix ? 1 : p.a.kv.n_seqs; }
+
+// Pair `tile` of that sequence.
+__device__ __forceinline__ void pair_work(const TcAttnParams& p, int b, const TcSeq& q, int tile, TcWork& w) {
+    const KvView& kv = p.a.kv;
+    const int pair = 2 * p.tile_tokens;
+    const int64_t most = kv.table_stride << kv.page_shift;
+    w.b = b;
+    w.t0 = q.t0 + tile * pair;
+    w.tokens = q.tokens - tile * pair < pair ? q.tokens - tile * pair : pair;
+    if (p.prefix) {
+        w.pos0 = w.lo = w.sinks = w.sink_blocks = 0;
+        w.end = int(p.a.shared_len < most ? p.a.shared_len : most);
+        w.blocks = (w.end + kKeys - 1) / kKeys;
+        return;
+    }
+    if (q.len > most) atomicOr(kv.err, kErrRange);
+    const int64_t pos0 = int64_t(q.len) - q.tokens + tile * pair;
+    int64_t end = pos0 + w.tokens;  // one past the last token's position
+    if (end > most) end = most;
+    if (end < 0) end = 0;
+    int64_t lo = p.a.window > 0 && pos0 + 1 > p.a.window ? pos0 + 1 - p.a.window : 0;
+    int64_t sinks = p.a.sinks < lo ? p.a.sinks : lo;
+    if (p.a.shared_len > 0) sinks = 0, lo = lo > p.a.shared_len ? lo : p.a.shared_len;
+    if (sinks > end) sinks = end;
+    if (lo > end) lo = end;
+    w.pos0 = int(pos0);
+    w.end = int(end);
+    w.lo = int(lo);
+    w.sinks = int(sinks);
+    w.sink_blocks = (w.sinks + kKeys - 1) / kKeys;
+    w.blocks = w.sink_blocks + (w.end > w.lo ? (w.end + kKeys - 1) / kKeys - w.lo / kKeys : 0);
+}
+
 // The tile pair with the given number, counted over all sequences (a sequence
 // of n tokens has ceil(n / pair)); false: there is none.  One warp finds it,
 // 32 sequences at a time.
 __device__ __forceinline__ bool find_pair(const TcAttnParams& p, int number, int lane, TcWork& w) {
-    const KvView& kv = p.a.kv;
-    const int pair = 2 * p.tile_tokens;
-    const int total = kv.q_start[kv.n_seqs] < p.a.n_tokens ? kv.q_start[kv.n_seqs] : p.a.n_tokens;
-    if (p.prefix) {
-        w.b = 0;
-        w.t0 = number * pair;
-        w.tokens = total - w.t0 < pair ? total - w.t0 : pair;
-        if (w.tokens <= 0) return false;
-        w.pos0 = 0;
-        w.lo = w.sinks = w.sink_blocks = 0;
-        const int64_t most = kv.table_stride << kv.page_shift;
-        w.end = int(p.a.shared_len < most ? p.a.shared_len : most);
-        w.blocks = (w.end + kKeys - 1) / kKeys;
-        return true;
-    }
+    const int pair = 2 * p.tile_tokens, seqs = tc_seqs(p);
     int base = 0;
-    for (int b0 = 0; b0 < kv.n_seqs; b0 += 32) {
+    for (int b0 = 0; b0 < seqs; b0 += 32) {
         const int b = b0 + lane;
-        int n = 0, t0 = 0;
-        if (b < kv.n_seqs) {
-            t0 = kv.q_start[b];
-            n = kv.q_start[b + 1] - t0;
-            if (n < 0 || t0 < 0 || t0 + n > p.a.n_tokens) n = 0;
-        }
-        const int tiles = (n + pair - 1) / pair;
+        TcSeq q = {0, 0, 0};
+        if (b < seqs) q = tc_seq(p, b);
+        const int tiles = (q.tokens + pair - 1) / pair;
         int incl = tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -282,30 +324,112 @@ __device__ __forceinline__ bool find_pair(const TcAttnParams& p, int number, int
         }
         const int src = __ffs(hit) - 1;
         const int before = base + __shfl_sync(0xffffffffu, incl - tiles, src);
-        n = __shfl_sync(0xffffffffu, n, src);
-        t0 = __shfl_sync(0xffffffffu, t0, src);
-        const int tile = number - before;
-        w.b = b0 + src;
-        w.t0 = t0 + tile * pair;
-        w.tokens = n - tile * pair < pair ? n - tile * pair : pair;
-        const int64_t len = kv.kv_len[w.b], most = kv.table_stride << kv.page_shift;
-        if (len > most) atomicOr(kv.err, kErrRange);
-        const int64_t pos0 = len - n + tile * pair;
-        int64_t end = pos0 + w.tokens;  // one past the last token's position
-        if (end > most) end = most;
-        if (end < 0) end = 0;
-        int64_t lo = p.a.window > 0 && pos0 + 1 > p.a.window ? pos0 + 1 - p.a.window : 0;
-        int64_t sinks = p.a.sinks < lo ? p.a.sinks : lo;
-        if (p.a.shared_len > 0) sinks = 0, lo = lo > p.a.shared_len ? lo : p.a.shared_len;
-        if (sinks > end) sinks = end;
-        if (lo > end) lo = end;
-        w.pos0 = int(pos0);
-        w.end = int(end);
-        w.lo = int(lo);
-        w.sinks = int(sinks);
-        w.sink_blocks = (w.sinks + kKeys - 1) / kKeys;
-        w.blocks = w.sink_blocks + (w.end > w.lo ? (w.end + kKeys - 1) / kKeys - w.lo / kKeys : 0);
+        q.t0 = __shfl_sync(0xffffffffu, q.t0, src);
+        q.tokens = __shfl_sync(0xffffffffu, q.tokens, src);
+        q.len = __shfl_sync(0xffffffffu, q.len, src);
+        pair_work(p, b0 + src, q, number - before, w);
         return true;
+    }
+    return false;
+}
+
+// Ranges: the blocks of all pairs and key heads form one line, in the order of
+// sequences, pairs and heads (a pair without blocks counts for one, so that its
+// rows are written), and each CTA takes `share` of them, whatever the pairs'
+// lengths.  Before its blocks every pair has kFixed places for its fixed cost:
+// without them the CTA whose range held the first pairs of a prompt, of a block
+// or two each, took twice as long as the others.  Places of one head of a
+// sequence, and the most blocks that a pair has:
+__device__ __forceinline__ int seq_blocks(const TcAttnParams& p, int b, const TcSeq& q, int lane, int& most) {
+    const int pair = 2 * p.tile_tokens, tiles = (q.tokens + pair - 1) / pair;
+    int sum = 0;
+    for (int i = lane; i < tiles; i += 32) {
+        TcWork w;
+        pair_work(p, b, q, i, w);
+        const int n = w.blocks > 0 ? w.blocks : 1;
+        sum += kFixed + n;
+        most = most > n ? most : n;
+    }
+    return __reduce_add_sync(0xffffffffu, sum);
+}
+struct Range {
+    int64_t begin;  // of the pair (and head) in work, on the line
+    int64_t share, left;
+    int b, tile, tiles, i;  // the sequence, its pair, how many it has, and the pair's next place
+    TcSeq q;
+    TcWork w;
+};
+// The next pair that has tokens, from (b, tile) on; false: the line ends.
+__device__ __forceinline__ bool range_pair(const TcAttnParams& p, Range& r) {
+    const int pair = 2 * p.tile_tokens, seqs = tc_seqs(p);
+    while (r.tile >= r.tiles) {
+        if (++r.b >= seqs) return false;
+        r.q = tc_seq(p, r.b);
+        r.tile = 0;
+        r.tiles = (r.q.tokens + pair - 1) / pair;
+    }
+    pair_work(p, r.b, r.q, r.tile, r.w);
+    return true;
+}
+// This CTA's range.
+__device__ __forceinline__ void open_range(const TcAttnParams& p, int lane, Range& r) {
+    const int seqs = tc_seqs(p), heads = p.a.kv.n_heads;
+    int64_t U = 0;
+    int most = 1;
+    for (int b = 0; b < seqs; ++b) U += int64_t(seq_blocks(p, b, tc_seq(p, b), lane, most)) * heads;
+    most = __reduce_max_sync(0xffffffffu, most);
+    // a pair of n blocks lies in at most n / share + 2 ranges: its slots hold them
+    r.share = (U + gridDim.x - 1) / gridDim.x;
+    const int64_t least = (most + p.slots - 3) / (p.slots - 2);
+    if (r.share < least) r.share = least;
+    if (r.share < kMinPart) r.share = kMinPart;
+    const int64_t from = int64_t(blockIdx.x) * r.share;
+    r.left = U - from < r.share ? U - from : r.share;
+    if (r.left <= 0) return;
+    r.begin = 0;
+    for (r.b = 0;; ++r.b) {
+        r.q = tc_seq(p, r.b);
+        const int64_t n = int64_t(seq_blocks(p, r.b, r.q, lane, most)) * heads;
+        if (from < r.begin + n) break;
+        r.begin += n;
+    }
+    r.tiles = (r.q.tokens + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+    for (r.tile = 0;; ++r.tile) {
+        pair_work(p, r.b, r.q, r.tile, r.w);
+        const int64_t n = int64_t(kFixed + (r.w.blocks > 0 ? r.w.blocks : 1)) * heads;
+        if (from < r.begin + n) break;
+        r.begin += n;
+    }
+    const int units = kFixed + (r.w.blocks > 0 ? r.w.blocks : 1);
+    r.w.hk = int((from - r.begin) / units);
+    r.begin += int64_t(r.w.hk) * units;
+    r.i = int(from - r.begin);
+}
+// The next piece of it that has blocks (or is a pair without any).
+__device__ __forceinline__ bool take_range(const TcAttnParams& p, Range& r, TcWork& w) {
+    while (r.left > 0) {
+        const int units = kFixed + (r.w.blocks > 0 ? r.w.blocks : 1);
+        const int n = units - r.i < r.left ? units - r.i : int(r.left);
+        const int from = r.i > kFixed ? r.i - kFixed : 0, to = r.i + n - kFixed;
+        w = r.w;
+        w.i0 = from;
+        w.nb = w.blocks > 0 ? to - from : 0;
+        const int64_t first = (r.begin + kFixed) / r.share;
+        w.split = int(blockIdx.x - first);
+        w.parts = int((r.begin + units - 1) / r.share - first) + 1;
+        r.left -= n;
+        r.i += n;
+        if (r.i == units && r.left > 0) {
+            r.begin += units;
+            r.i = 0;
+            if (++r.w.hk == p.a.kv.n_heads) {
+                ++r.tile;
+                const bool some = range_pair(p, r);
+                r.w.hk = 0;
+                if (!some) r.left = 0;
+            }
+        }
+        if (to > from) return true;
     }
     return false;
 }
@@ -317,17 +441,9 @@ __device__ __forceinline__ bool block_has_unseen(const TcWork& w, int i) {
     return j0 < lo || j0 + kKeys > hi;
 }
 __device__ __forceinline__ int count_pairs(const TcAttnParams& p, int lane) {
-    const KvView& kv = p.a.kv;
-    const int pair = 2 * p.tile_tokens;
-    if (p.prefix) {
-        const int total = kv.q_start[kv.n_seqs] < p.a.n_tokens ? kv.q_start[kv.n_seqs] : p.a.n_tokens;
-        return (total + pair - 1) / pair;
-    }
+    const int pair = 2 * p.tile_tokens, seqs = tc_seqs(p);
     int sum = 0;
-    for (int b = lane; b < kv.n_seqs; b += 32) {
-        const int t0 = kv.q_start[b], n = kv.q_start[b + 1] - t0;
-        if (n > 0 && t0 >= 0 && t0 + n <= p.a.n_tokens) sum += (n + pair - 1) / pair;
-    }
+    for (int b = lane; b < seqs; b += 32) sum += (tc_seq(p, b).tokens + pair - 1) / pair;
     return __reduce_add_sync(0xffffffffu, sum);
 }
 
@@ -369,9 +485,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     uint64_t* o_empty = o_full + 2;
     uint64_t* w_full = o_empty + 2;     // per entry of `work`
     uint64_t* w_empty = w_full + 2;
-    TcWork* work = reinterpret_cast<TcWork*>(w_empty + 2);  // [2]: pairs in hand; tokens 0: no more
+    uint64_t* w_taken = w_empty + 2;    // a pair's copies are nearly all on their way
+    TcWork* work = reinterpret_cast<TcWork*>(w_taken + 1);  // [2]: pairs in hand; tokens 0: no more
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(work + 2);
-    static_assert((2 + 3 * NS + 2 + 4 + 2 + 2 + 2 + 2) * 8 + 2 * sizeof(TcWork) + 4 <= 640, "barriers and work entries");
+    static_assert((2 + 3 * NS + 2 + 4 + 2 + 2 + 2 + 2 + 1) * 8 + 2 * sizeof(TcWork) + 4 <= 640, "barriers and work entries");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KvView& kv = p.a.kv;
@@ -379,6 +496,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
+        mbar_init(w_taken, 1);
         for (int i = 0; i < NS; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&clean[i], 1);
@@ -391,7 +509,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
             mbar_init(&w_full[i], 1);
-            mbar_init(&w_empty[i], kSoftmaxWarps + 2);
+            mbar_init(&w_empty[i], kSoftmaxWarps + 3);
         }
         fence_barrier_init();
         prefetch_map(&p.q_map);
@@ -414,39 +532,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kSoftmaxWarps + 1) {
-            // ---- producer: the pairs, and of each Q, then K and V of its blocks
+            // ---- producer: of each pair Q, then K and V of its blocks
             const int page_keys = (1 << kv.page_shift) < kKeys ? (1 << kv.page_shift) : kKeys;
             const int boxes = kKeys / page_keys;  // of a block (at most 8)
-            const int pairs = count_pairs(p, lane);
             RingPos at;
             int64_t issued = 0;
             bool ok = true;
             int quse = 0;
             for (int n = 0; ok; ++n) {
-                if (n >= 2 && !(ok = warp_wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, kv.err, kErrTimeoutEmpty))) break;
-                int item = int(blockIdx.x);
-                if (n > 0) {
-                    if (lane == 0) item = int(gridDim.x + atomicAdd(p.counter, 1u));
-                    item = __shfl_sync(0xffffffffu, item, 0);
-                }
-                TcWork w;
-                const int number = item / (kv.n_heads * p.splits), rest = item - number * (kv.n_heads * p.splits);
-                // the pairs with the most keys (the last of a sequence) first
-                const bool more = number < pairs && find_pair(p, pairs - 1 - number, lane, w);
-                if (!more) w.tokens = 0;
-                w.hk = rest / p.splits;
-                w.split = rest - w.hk * p.splits;
-                // parts of at least kMinPart blocks; the others are empty
-                w.parts = more ? w.blocks / kMinPart : 1;
-                w.parts = w.parts < 1 ? 1 : w.parts < p.splits ? w.parts : p.splits;
-                const bool in = more && w.split < w.parts;
-                w.i0 = in ? int(int64_t(w.blocks) * w.split / w.parts) : 0;
-                w.nb = in ? int(int64_t(w.blocks) * (w.split + 1) / w.parts) - w.i0 : 0;
+                if (!(ok = warp_wait(&w_full[n & 1], (n >> 1) & 1, kv.err, kErrTimeoutFull))) break;
+                const TcWork w = work[n & 1];
+                __syncwarp();
                 if (lane == 0) {
-                    work[n & 1] = w;
-                    mbar_arrive(&w_full[n & 1]);
+                    mbar_arrive(&w_empty[n & 1]);
+                    if (w.nb == 0) mbar_arrive(w_taken);
                 }
-                if (!more) break;
+                if (w.tokens == 0) break;
                 if (w.nb == 0) continue;
                 const int tiles = w.tokens > p.tile_tokens ? 2 : 1;
                 if (quse > 0 && !(ok = warp_wait(q_empty, (quse - 1) & 1, kv.err, kErrTimeoutEmpty))) break;
@@ -486,6 +587,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         ++issued;
                         at.template next<NS>();
                     }
+                    if (lane == 0 && i == w.i0 + (w.nb > 1 ? w.nb - 2 : 0)) mbar_arrive(w_taken);  // (one block is left)
                 }
             }
             // keep the CTA alive until every copy it issued has landed
@@ -493,6 +595,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 if (quse > 0) mbar_wait_bounded(q_full, (quse - 1) & 1, kWaitNs, kv.err, kErrTimeoutDrain);
                 for (int64_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
                     mbar_wait_bounded(&kv_full[i % NS], (i / NS) & 1, kWaitNs, kv.err, kErrTimeoutDrain);
+            }
+        } else if (warp == kSoftmaxWarps + 3) {
+            // ---- scheduler.  Pairs from the counter are taken when the one
+            // before is nearly all on its way, not earlier: a CTA with a long pair in
+            // work would sit on another.
+            const int pairs = p.slots == 0 ? count_pairs(p, lane) : 0;
+            Range r;
+            if (p.slots > 0) open_range(p, lane, r);
+            for (int n = 0;; ++n) {
+                if (n >= 2 && !warp_wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, kv.err, kErrTimeoutEmpty)) break;
+                TcWork w;
+                bool more;
+                if (p.slots > 0) {
+                    more = take_range(p, r, w);
+                } else {
+                    int item = int(blockIdx.x);
+                    if (n > 0) {
+                        if (!warp_wait(w_taken, (n - 1) & 1, kv.err, kErrTimeoutEmpty)) break;
+                        if (lane == 0) item = int(gridDim.x + atomicAdd(p.counter, 1u));
+                        item = __shfl_sync(0xffffffffu, item, 0);
+                    }
+                    // the pairs with the most keys (the last of a sequence) first
+                    const int number = item / kv.n_heads;
+                    more = number < pairs && find_pair(p, pairs - 1 - number, lane, w);
+                    w.hk = item - number * kv.n_heads;
+                    w.split = w.i0 = 0;
+                    w.parts = 1;
+                    w.nb = w.blocks;
+                }
+                if (!more) w.tokens = w.nb = 0;
+                if (lane == 0) {
+                    work[n & 1] = w;
+                    mbar_arrive(&w_full[n & 1]);
+                }
+                __syncwarp();
+                if (!more) break;
             }
         } else if (warp == kSoftmaxWarps) {
             // ---- MMA issuer
@@ -750,16 +888,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 if (!(ok = warp_wait(&o_full[t], (blocks - 1) & 1, kv.err, kErrTimeoutMma))) break;
                 tc_after();
             }
-            // a row whose keys were all here goes to the output, others to their part;
-            // an empty part has nothing to say but its log
+            // a row whose keys were all here goes to the output, others to their part
             const int split = w.split;
             const bool to_part = p.part_o && (p.prefix || p.tails || w.parts > 1);
             const int64_t row = int64_t(w.t0 + tok) * p.a.n_q_heads + w.hk * group + head;
             const int64_t part = int64_t(split) * p.a.n_tokens * p.a.n_q_heads + row;
             const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if (live && p.part_o) p.part_lse[part] = to_part || split > 0 ? lse2 : kWritten;
-            if (split == 0 || nb > 0) {
+            if (live && p.part_o) {
+                p.part_lse[part] = to_part ? lse2 : kWritten;
+                if (to_part && split == w.parts - 1)  // the row has no further parts
+                    for (int e = w.parts; e < p.slots; ++e) p.part_lse[part + (e - split) * int64_t(p.a.n_tokens) * p.a.n_q_heads] = -INFINITY;
+            }
+            {
                 if (live && !to_part && p.a.lse) p.a.lse[row] = lse2 * 0.6931471805599453f;
                 uint8_t* stage = outs + warp * 4096;
                 if (to_part) write_rows<DIM>(p.part_o, part * DIM, live, oa, nb > 0, inv, stage, lane, &o_empty[t]);
@@ -864,7 +1005,7 @@ bool encode(CUtensorMap* m, bool f16, const void* ptr, int rank, const int64_t* 
 }
 
 template <typename T, int DIM>
-cudaError_t launch_tc(const AttnParams& a, bool prefix, int splits, float* part_o, float* part_lse, unsigned* counter,
+cudaError_t launch_tc(const AttnParams& a, bool prefix, int slots, float* part_o, float* part_lse, unsigned* counter,
                       int sm_count, cudaStream_t s) {
     static bool ready[64] = {false};
     int dev = 0;
@@ -881,7 +1022,7 @@ cudaError_t launch_tc(const AttnParams& a, bool prefix, int splits, float* part_
     p.a = a;
     p.prefix = prefix ? 1 : 0;
     p.tails = !prefix && a.shared_len > 0 ? 1 : 0;
-    p.splits = splits;
+    p.slots = slots;
     p.part_o = part_o;
     p.part_lse = part_lse;
     p.counter = counter;
@@ -892,8 +1033,8 @@ cudaError_t launch_tc(const AttnParams& a, bool prefix, int splits, float* part_
     const int qb[3] = {64, group, p.tile_tokens};
     if (!encode_cache_maps(f16, a.kv, kKeys, &p.k_map, &p.v_map) || !encode(&p.q_map, f16, a.q, 3, qd, qs, qb))
         return cudaErrorInvalidValue;
-    const int64_t items = tc_pairs(a.n_tokens, group, a.kv.n_seqs, prefix) * a.kv.n_heads * splits;
-    return launch_serial(attn_tc_kernel<T, DIM>, dim3(unsigned(items < sm_count ? items : sm_count)), kTcThreads,
+    const int64_t items = tc_pairs(a.n_tokens, group, a.kv.n_seqs, prefix) * a.kv.n_heads;
+    return launch_serial(attn_tc_kernel<T, DIM>, dim3(unsigned(slots == 0 && items < sm_count ? items : sm_count)), kTcThreads,
                          TcGeom<DIM>::kSmem, s, p);
 }
 
@@ -913,13 +1054,13 @@ int64_t tc_pairs(int64_t n_tokens, int group, int n_seqs, bool prefix) {
     return prefix || n_seqs == 1 ? (n_tokens + pair - 1) / pair : n_tokens / pair + (n_seqs < n_tokens ? n_seqs : n_tokens);
 }
 
-cudaError_t launch_attn_tc(int dtype, const AttnParams& a, bool prefix, int splits, float* part_o, float* part_lse,
+cudaError_t launch_attn_tc(int dtype, const AttnParams& a, bool prefix, int slots, float* part_o, float* part_lse,
                            unsigned* counter, int sm_count, cudaStream_t s) {
     if (a.kv.head_dim == 128)
-        return dtype == QX_F16 ? launch_tc<__half, 128>(a, prefix, splits, part_o, part_lse, counter, sm_count, s)
-                               : launch_tc<__nv_bfloat16, 128>(a, prefix, splits, part_o, part_lse, counter, sm_count, s);
-    return dtype == QX_F16 ? launch_tc<__half, 64>(a, prefix, splits, part_o, part_lse, counter, sm_count, s)
-                           : launch_tc<__nv_bfloat16, 64>(a, prefix, splits, part_o, part_lse, counter, sm_count, s);
+        return dtype == QX_F16 ? launch_tc<__half, 128>(a, prefix, slots, part_o, part_lse, counter, sm_count, s)
+                               : launch_tc<__nv_bfloat16, 128>(a, prefix, slots, part_o, part_lse, counter, sm_count, s);
+    return dtype == QX_F16 ? launch_tc<__half, 64>(a, prefix, slots, part_o, part_lse, counter, sm_count, s)
+                           : launch_tc<__nv_bfloat16, 64>(a, prefix, slots, part_o, part_lse, counter, sm_count, s);
 }
 
 cudaError_t launch_attn_join(int dtype, const JoinParams& p, cudaStream_t s) {

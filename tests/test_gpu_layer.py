@@ -127,6 +127,23 @@ def test_prefill_of_more_tiles_than_the_gpu_holds(heads, window, sinks):
     b.check(out, lse, b.expect(dim ** -0.5, window, sinks), f"{heads} window {window}")
 
 
+@pytest.mark.parametrize("heads", [(32, 8, 128), (14, 2, 64), (6, 6, 64), (16, 1, 128)])
+@pytest.mark.parametrize("q_lens,kv_lens", [
+    ([100, 0, 37, 200, 130], [4000, 60, 37, 2100, 90]),  # an idle sequence; one with 40 padding tokens
+    ([129], [6000]), ([33] * 20, list(range(33, 1733, 85))), ([400, 300], [3, 2000])])
+def test_few_pairs_over_long_contexts(heads, q_lens, kv_lens):
+    """Key blocks shared out over the SMs: rows in several parts, in one, and in none."""
+    hq, hkv, dim = heads
+    for i, (window, sinks) in enumerate([(0, 0), (1800, 5), (1500, 0)]):
+        b = Batch(q_lens, kv_lens, hq, hkv, dim, (16, 64, 256)[i], (BF16, F16, BF16)[i], ("hnd", "nhd", "hnd")[i], seed=20 + i)
+        lse = torch.full((b.T, hq), 7.0, device="cuda")
+        out = torch.full((b.T, hq, dim), float("nan"), dtype=(b.dtype, F32, b.dtype)[i], device="cuda")
+        exp = b.expect(dim ** -0.5, window, sinks)
+        for _ in range(2):
+            qx.qx_attn_paged(b.kv, b.q, window=window, sinks=sinks, out=out, lse=lse)
+            b.check(out, lse, exp, f"{heads} window {window} sinks {sinks}")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("q_lens,kv_lens", [([1], [5000]), ([300], [2500]), ([1, 1, 200], [3000, 1, 900])])
 @pytest.mark.parametrize("std", [0.0, 1.0, 30.0])
