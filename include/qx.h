@@ -20,6 +20,12 @@
  * cores (llamay, section "CUDA": a tensor-core prefill kernel, whose missing
  * piece was staging the next weight tile behind the current multiply).
  *
+ * And it runs what stands between those products in a decoder layer: rotated
+ * keys and values appended to a paged cache (qx_rope_append), attention over
+ * it (qx_attn_paged, qx_attn_shared) and the norms around a block
+ * (qx_block_norm).  Their activations are f32, f16 or bf16, their caches f16 or
+ * bf16; the pages have no counterpart of them.
+ *
  * Conventions shared by every entry point:
  *   - Weights are a row-major array of blocks; row r starts at byte
  *     r * qx_row_bytes(fmt, cols).  Block layouts are the GGUF ones:
@@ -42,13 +48,17 @@
  *     return before anything is launched or written; a failed launch returns
  *     QX_ERR_CUDA.
  *   - Alignment: W, the f32 activation x and the qx_act_q8 buffers must be
- *     16-byte aligned; the outputs y, Y and P 4-byte aligned.
+ *     16-byte aligned; the outputs y, Y and P 4-byte aligned.  q, k, v, the
+ *     cache, cos, sin and the outputs of the rotation and attention calls must
+ *     be 16-byte aligned with strides that are multiples of 8 elements; the
+ *     operands of qx_block_norm need only their elements' alignment.
  *   - Only compute capability 10.3 (GB300) is served.  Any other device is
  *     declined with QX_ERR_UNSUPPORTED_DEVICE rather than run through another
  *     kernel (llamay, section "CUDA": below its minimum capability the
  *     backend declines at open with a message naming the reason).
  *   - Kernels bound every wait.  A wait that runs out sets a device error
- *     word and the kernel returns; qx_device_check() reports it.
+ *     word and the kernel returns; qx_device_check() reports it, and pages,
+ *     lengths and positions out of range too.
  */
 #ifndef QX_H
 #define QX_H
@@ -370,7 +380,7 @@ typedef struct {
     int head_dim;         /* a multiple of 8, at most QX_MAX_HEAD_DIM           */
     int page_size;        /* a power of two, 16 .. 65536                        */
     int64_t n_pages;
-    int64_t page_stride;  /* elements, multiples of 8; k and v 16-byte aligned  */
+    int64_t page_stride;  /* elements, multiples of 8, at least head_dim        */
     int64_t head_stride;
     int64_t slot_stride;
     const int32_t* table;

@@ -27,7 +27,8 @@ BAD_KV = [(dict(k=None), "ARG"), (dict(v=None), "ARG"), (dict(table=None), "ARG"
           (dict(head_dim=0), "SHAPE"), (dict(head_dim=60), "SHAPE"), (dict(head_dim=264), "SHAPE"), (dict(page_size=8), "SHAPE"),
           (dict(page_size=48), "SHAPE"), (dict(page_size=1 << 17), "SHAPE"), (dict(n_pages=0), "SHAPE"),
           (dict(n_pages=1 << 31), "SHAPE"), (dict(table_stride=0), "SHAPE"), (dict(n_seqs=0), "SHAPE"),
-          (dict(page_stride=-8), "SHAPE"), (dict(slot_stride=1 << 41), "SHAPE"), (dict(slot_stride=68), "ALIGN"),
+          (dict(page_stride=-8), "SHAPE"), (dict(slot_stride=1 << 41), "SHAPE"), (dict(slot_stride=56), "SHAPE"),
+          (dict(head_stride=0), "SHAPE"), (dict(page_stride=8), "SHAPE"), (dict(slot_stride=68), "ALIGN"),
           (dict(head_stride=1001), "ALIGN"), (dict(k=A16 + 8), "ALIGN"), (dict(v=A16 + 2), "ALIGN")]
 
 
@@ -73,7 +74,7 @@ def test_attention_refusals(lib):
     for shared in (False, True):
         for bad in (dict(q=None), dict(out=None), dict(scratch=None), dict(window=-1), dict(scale=float("inf")), dict(scale=float("nan"))):
             assert call(shared, **bad) == qx.QX_ERR_ARG, bad
-        for bad in (dict(hq=3), dict(hq=0), dict(hq=2 * 129), dict(n=-1), dict(n=1 << 31), dict(stride=-8)):
+        for bad in (dict(hq=3), dict(hq=0), dict(hq=2 * 129), dict(n=-1), dict(n=1 << 31), dict(stride=-8), dict(n=2, stride=248)):
             assert call(shared, **bad) == qx.QX_ERR_SHAPE, bad
         for bad in (dict(dtype=qx.QX_F16), dict(dtype=3)):
             assert call(shared, **bad) == qx.QX_ERR_FMT, bad
