@@ -393,15 +393,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     uint64_t* empty = full + NS;
     int64_t* scan = reinterpret_cast<int64_t*>(empty + NS);  // [8]
     Cursor* start = reinterpret_cast<Cursor*>(scan + 2 * kSplitWarps);
-    UnitInfo* info = reinterpret_cast<UnitInfo*>(start + 1);  // [NS], and the first unit's
-    int* last_flag = reinterpret_cast<int*>(info + NS + 1);
-    static_assert((2 * NS + 2 * kSplitWarps) * 8 + sizeof(Cursor) + (NS + 1) * sizeof(UnitInfo) + 4 <= G::kMisc,
+    UnitInfo* info = reinterpret_cast<UnitInfo*>(start + 1);  // [NS]
+    int* last_flag = reinterpret_cast<int*>(info + NS);
+    static_assert((2 * NS + 2 * kSplitWarps) * 8 + sizeof(Cursor) + NS * sizeof(UnitInfo) + 4 <= G::kMisc,
                   "barriers, units and the worker's place");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 2);  // the copies, and the description
             mbar_init(&empty[i], kSplitWarps);
         }
         fence_barrier_init();
@@ -487,7 +487,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         x.parts = int(wl - wf);
         x.part = 2 * int(wf) + (begin_of(wf) < begin ? 1 : 0);
     };
-    if (threadIdx.x == 0) describe(*start, int(first - start->begin), info[NS]);
 
     if (warp >= kSplitWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
@@ -515,31 +514,33 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         for (; left > 0; --left) {
             int lo, hi;
             const int j0 = unit_keys(cur.w, ui, lo, hi);
-            const int in_page = (j0 + lane * page_keys) & in_page_mask, hk = cur.hk, now = page;
-            UnitInfo x;
-            describe(cur, ui, x);
-            if (left > 1) {  // the next unit's pages are looked up while this one's room is awaited
+            const int in_page = (j0 + lane * page_keys) & in_page_mask;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[slot], phase, kSplitWaitNs, p.kv.err, kErrTimeoutEmpty));
+            if (!ok) break;
+            const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(live) * page_keys * 128 * G::kPanels * 2);
+            __syncwarp();
+            if (page >= 0) {
+                uint8_t* dst = smem + slot * 2 * G::kHalfStage + lane * page_keys * 128;
+#pragma unroll
+                for (int c = 0; c < G::kPanels; ++c) {
+                    tma_load_4d(dst + c * G::kPanelBytes, &pp.k_map, 64 * c, in_page, cur.hk, page, &full[slot]);
+                    tma_load_4d(dst + G::kHalfStage + c * G::kPanelBytes, &pp.v_map, 64 * c, in_page, cur.hk, page, &full[slot]);
+                }
+            }
+            if (lane == 0) {  // while they are on their way
+                UnitInfo x;
+                describe(cur, ui, x);
+                info[slot] = x;
+                mbar_arrive(&full[slot]);
+            }
+            __syncwarp();
+            if (left > 1) {  // the next unit's pages are looked up while its room is awaited
                 if (++ui == cur.w.units) {
                     next_tile(p, cur, group, B);
                     ui = 0;
                 }
                 page = page_for(ui);
-            }
-            const unsigned live = __ballot_sync(0xffffffffu, now >= 0);
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[slot], phase, kSplitWaitNs, p.kv.err, kErrTimeoutEmpty));
-            if (!ok) break;
-            if (lane == 0) {
-                info[slot] = x;
-                mbar_arrive_expect_tx(&full[slot], __popc(live) * page_keys * 128 * G::kPanels * 2);
-            }
-            __syncwarp();
-            if (now >= 0) {
-                uint8_t* dst = smem + slot * 2 * G::kHalfStage + lane * page_keys * 128;
-#pragma unroll
-                for (int c = 0; c < G::kPanels; ++c) {
-                    tma_load_4d(dst + c * G::kPanelBytes, &pp.k_map, 64 * c, in_page, hk, now, &full[slot]);
-                    tma_load_4d(dst + G::kHalfStage + c * G::kPanelBytes, &pp.v_map, 64 * c, in_page, hk, now, &full[slot]);
-                }
             }
             if (used < NS) ++used;
             if (++slot == NS) {
@@ -593,8 +594,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         pos_first = __reduce_min_sync(0xffffffffu, low);
         pos_last = __reduce_max_sync(0xffffffffu, high);
     };
-    consumers_sync();  // the first unit's description
-    open_tile(info[NS]);
+    {
+        UnitInfo x;
+        x.t0 = start->w.t0, x.pos0 = start->w.pos0, x.hk = start->hk;
+        x.r0 = kRows * start->rt, x.rows = start->w.tokens * group - x.r0;
+        x.flags = start->b == p.kv.n_seqs ? kPrefix : 0;
+        open_tile(x);
+    }
     float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(p.scratch) + kCounterBytes);
     unsigned* counters = static_cast<unsigned*>(p.scratch);
     const int window = p.window > 0 && p.window < INT32_MAX ? int(p.window) : INT32_MAX;
