@@ -939,8 +939,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (row >= rows) return;
-    if (seq_of_token(p.a.kv, int(row / p.a.n_q_heads)) < 0) return;
     const float mine = lane < p.parts ? p.part_lse[lane * rows + row] : -INFINITY;
+    if (int(row / p.a.n_q_heads) >= p.a.kv.q_start[p.a.kv.n_seqs]) return;  // a token of no sequence
     if (__shfl_sync(0xffffffffu, mine, 0) == kWritten) return;
     float M = mine;
 #pragma unroll
@@ -950,17 +950,32 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     float acc[V] = {};
-    for (int i = 0; i < p.parts; ++i) {
-        const float c = __shfl_sync(0xffffffffu, wt, i);
-        if (c == 0.0f) continue;  // (an empty part's o is not written)
-        const float* src = p.part_o + (i * rows + row) * DIM + V * lane;
-        if constexpr (V == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            acc[0] += c * v.x, acc[1] += c * v.y, acc[2] += c * v.z, acc[3] += c * v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
-            acc[0] += c * v.x, acc[1] += c * v.y;
+    // the parts that say something, four loads in flight
+    for (unsigned left = __ballot_sync(0xffffffffu, wt != 0.0f); left != 0;) {
+        float v[4][V], c[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int i = left ? __ffs(left) - 1 : 0;
+            c[y] = __shfl_sync(0xffffffffu, wt, i);
+            if (!left) c[y] = 0.0f;
+#pragma unroll
+            for (int x = 0; x < V; ++x) v[y][x] = 0.0f;
+            const float* src = p.part_o + (i * rows + row) * DIM + V * lane;
+            if (left) {
+                if constexpr (V == 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(src);
+                    v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
+                } else {
+                    const float2 f = *reinterpret_cast<const float2*>(src);
+                    v[y][0] = f.x, v[y][1] = f.y;
+                }
+            }
+            left &= left - 1;
         }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int x = 0; x < V; ++x) acc[x] += c[y] * v[y][x];
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
