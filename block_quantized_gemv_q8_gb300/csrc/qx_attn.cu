@@ -615,12 +615,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
-    // (after a wait that ran out the rest runs through without waiting, for the barriers' sake)
+    // A wait that runs out ends the consumers: all four wait for the same copies
+    // and for the same time, so they end together, and none is left at a barrier.
     const auto arrived = [&]() {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], phase, kSplitWaitNs, p.kv.err, kErrTimeoutFull));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], phase, kSplitWaitNs, p.kv.err, kErrTimeoutFull));
     };
     arrived();
-    for (; left > 0; --left) {
+    for (; left > 0 && ok; --left) {
         const int flags = info[slot].flags, lo = info[slot].lo, hi = info[slot].hi;
         const int j0 = info[slot].j0 + 16 * warp;  // this warp's sixteen keys
         if (flags & kOpens) {
@@ -730,7 +731,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         // are on their way while its warps are joined, eight rows at a time:
         // every warp leaves its (m, l, o), and every thread then joins some
         // elements.
-        if (left > 1) open_tile(info[slot]);
+        if (left > 1 && ok) open_tile(info[slot]);
         const int rows = done.rows;  // (16 at most count)
         const auto part_at = [&](int i) -> float* { return partials + int64_t(i) * partial_floats<DIM>(); };
         const auto finish = [&](int r, int d, float M, float L, float4 v) { write_four<T, DIM>(pp, done, r, d, M, L, v); };
