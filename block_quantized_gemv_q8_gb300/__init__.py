@@ -389,6 +389,7 @@ def qx_gemv_chain_noalloc(jobs, stream=None, marshalled=None):
     return jobs
 
 
+_F32 = torch.float32
 _DTYPE = {torch.float32: QX_F32, torch.float16: QX_F16, torch.bfloat16: QX_BF16}
 
 
@@ -485,18 +486,29 @@ def qx_rope_append(kv: PagedKV, q: torch.Tensor | None, k: torch.Tensor, v: torc
     cos, sin: float32 [positions, rot / 2] (None: no rotation); interleaved:
     pairs (2i, 2i + 1) instead of (i, i + rot / 2).  Returns the rotated
     queries in the cache's type."""
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k and v: need [tokens, heads, dim]")
     index, dim, dt = kv._index, kv.head_dim, k.dtype
     code = _DTYPE.get(dt)
     if code is None:
         raise TypeError(f"k: {dt} is not float32, float16 or bfloat16")
-    n = k.shape[0]
-    own = (n, kv.heads, dim)
-    k_stride, v_stride = _heads(k, own, dt, index, "k"), _heads(v, own, dt, index, "v")
+    shape = k.shape
+    n = shape[0]
+    (k_stride, kb, kc), (v_stride, vb, vc) = k.stride(), v.stride()
+    # (the common case in line: a call of a helper costs as much as its checks)
+    if not (shape == (n, kv.heads, dim) and v.shape == shape and v.dtype is dt and kb == vb == dim and kc == vc == 1
+            and k.get_device() == index and v.get_device() == index):
+        own = (n, kv.heads, dim)
+        k_stride, v_stride = _heads(k, own, dt, index, "k"), _heads(v, own, dt, index, "v")
     hq = q_ptr = q_stride = n_pos = half = 0
     out = cp = sp = None
     if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q: need [tokens, heads, dim]")
         hq = q.shape[1]
-        q_stride, q_ptr = _heads(q, (n, hq, dim), dt, index, "q"), q.data_ptr()
+        (q_stride, qb, qc), q_ptr = q.stride(), q.data_ptr()
+        if not (q.shape == (n, hq, dim) and q.dtype is dt and qb == dim and qc == 1 and q.get_device() == index):
+            q_stride = _heads(q, (n, hq, dim), dt, index, "q")
         if q_out is None:
             q_out = torch.empty((n, hq, dim), dtype=kv.dtype, device=kv.device)
         elif q_out.dtype != kv.dtype or q_out.shape != q.shape or not q_out.is_contiguous() or q_out.get_device() != index:
@@ -511,6 +523,8 @@ def qx_rope_append(kv: PagedKV, q: torch.Tensor | None, k: torch.Tensor, v: torc
             raise ValueError("cos and sin: need contiguous tensors on the cache's GPU")
         n_pos, half = cos.shape
         cp, sp = cos.data_ptr(), sin.data_ptr()
+    if n == 1:  # a single token's stride means nothing, and may be anything
+        k_stride = v_stride = q_stride = dim
     a = _PACK_QKV.pack(n, hq, code, q_ptr, k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride)
     st = lib().qx_rope_append(kv._ref, a, cp, sp, n_pos, 2 * half, 1 if interleaved else 0, out, _raw_stream(stream, index))
     if st:
@@ -611,28 +625,40 @@ def qx_block_norm(y: torch.Tensor | None, r: torch.Tensor, w_post: torch.Tensor 
     code, res_code = _DTYPE.get(act), _DTYPE.get(res)
     if code is None or res_code is None:
         raise TypeError("qx_block_norm takes float32, float16 and bfloat16")
-    r_stride = _rows(r, shape, res, index, "r")
+    # (the common case of each tensor in line: a call of a helper costs as much as its checks)
+    strides = r.stride()
+    r_stride = strides[0] if strides[1] == 1 else _rows(r, shape, res, index, "r")
     y_ptr = gate_ptr = post = pre = ro_ptr = x_ptr = y_stride = gate_stride = ro_stride = x_stride = 0
     if y is not None:
-        y_ptr, y_stride = y.data_ptr(), _rows(y, shape, act, index, "y")
+        strides, y_ptr = y.stride(), y.data_ptr()
+        y_stride = strides[0] if y.dtype is act and y.shape == shape and strides[1] == 1 and y.get_device() == index else \
+            _rows(y, shape, act, index, "y")
     if gate is not None:
         if gate.dim() == 1:
             gate_ptr = _vector(gate, cols, act, index, "gate")
         else:
             gate_ptr, gate_stride = gate.data_ptr(), _rows(gate, shape, act, index, "gate")
     if w_post is not None:
-        post = _vector(w_post, cols, torch.float32, index, "w_post")
+        post = w_post.data_ptr()
+        if not (w_post.dtype is _F32 and w_post.get_device() == index and w_post.shape == (cols,) and w_post.is_contiguous()):
+            _vector(w_post, cols, _F32, index, "w_post")
     if y is None and r_out is None:
         r_out = r  # unchanged
     else:
         if r_out is None:
             r_out = torch.empty(shape, dtype=res, device=r.device)
-        ro_ptr, ro_stride = r_out.data_ptr(), _rows(r_out, shape, res, index, "r_out")
+        strides, ro_ptr = r_out.stride(), r_out.data_ptr()
+        ro_stride = strides[0] if r_out.dtype is res and r_out.shape == shape and strides[1] == 1 and r_out.get_device() == index else \
+            _rows(r_out, shape, res, index, "r_out")
     if w_pre is not None:
-        pre = _vector(w_pre, cols, torch.float32, index, "w_pre")
+        pre = w_pre.data_ptr()
+        if not (w_pre.dtype is _F32 and w_pre.get_device() == index and w_pre.shape == (cols,) and w_pre.is_contiguous()):
+            _vector(w_pre, cols, _F32, index, "w_pre")
         if x_out is None:
             x_out = torch.empty(shape, dtype=act, device=r.device)
-        x_ptr, x_stride = x_out.data_ptr(), _rows(x_out, shape, act, index, "x_out")
+        strides, x_ptr = x_out.stride(), x_out.data_ptr()
+        x_stride = strides[0] if x_out.dtype is act and x_out.shape == shape and strides[1] == 1 and x_out.get_device() == index else \
+            _rows(x_out, shape, act, index, "x_out")
     else:
         x_out = None
     a = _PACK_NORM.pack(shape[0], cols, code, res_code, y_ptr, r.data_ptr(), gate_ptr, post, pre, alpha, eps, ro_ptr, x_ptr, y_stride,

@@ -387,6 +387,20 @@ def test_rope_append(src, dtype, hq, hkv, dim, rot, interleaved):
             assert (np.abs(got[ok] - want[ok]) <= bound(want[ok])).all()
 
 
+def test_rope_append_of_one_token_with_any_token_stride():
+    """One token's rows may be a view whose token stride is no multiple of 8."""
+    b = Batch([1], [30], 4, 2, 64, 16, F16)
+    base = torch.randn(9 * 512, device="cuda")
+    x = torch.as_strided(base, (1, 8, 64), (7, 64, 1))
+    cos, sin = table_of(32, 64)
+    q = qx.qx_rope_append(b.kv, x[:, :4], x[:, 4:6], x[:, 6:], cos, sin)
+    assert qx.qx_device_check() == qx.QX_OK
+    want = ref.rotate(ref.f64(base[:256].view(4, 64)), ref.f64(cos)[29], ref.f64(sin)[29], False)
+    assert (np.abs(ref.f64(q[0]) - want) <= 2.0 ** -11 * np.abs(want) + 2.0 ** -20).all()
+    got = ref.f64(b.v[int(b.table_host[0, 1]), :, 13])
+    assert (np.abs(got - ref.f64(base[384:512].view(2, 64))) <= 2.0 ** -11 * np.abs(got) + 2.0 ** -20).all()
+
+
 def test_rope_append_reports_what_is_out_of_range():
     b = Batch([1, 1], [20, 33], 4, 2, 64, 16, BF16)
     x = torch.randn(2, 8, 64, device="cuda")
