@@ -237,18 +237,25 @@ __device__ __forceinline__ void write_rows(T* dst, int64_t at, bool live, uint32
 
 // What a CTA works on: `tokens` tokens from t0 on (at most two tiles) of
 // sequence b, the first at position pos0, and the key blocks that any of its
-// rows sees: those of keys [0, sinks), then those of [lo, end).
+// rows sees: those of keys [0, sinks), then those of [lo, end).  In a kernel
+// for JOINT sinks, which lie in page 0 and pages are shorter than a block,
+// there is no block for them: page 0 stands in the first block of [lo, end)
+// for the page before lo's.
 struct TcWork {
     int b, t0, tokens, pos0, lo, end, sinks, sink_blocks, blocks;
     int hk, split, i0, nb;  // key head, part, and its blocks [i0, i0 + nb)
     int parts;              // parts of the pair's rows
+    int base;               // JOINT: key at which its blocks begin
 };
+template <bool JOINT>
 __device__ __forceinline__ int key_block(const TcWork& w, int i) {  // first key of the i-th block
+    if (JOINT) return w.base + i * kKeys;
     return (i < w.sink_blocks ? i : w.lo / kKeys + (i - w.sink_blocks)) * kKeys;
 }
+template <bool JOINT>
 __device__ __forceinline__ void key_range(const TcWork& w, int i, int& lo, int& hi) {  // keys of it that some row sees
-    lo = i < w.sink_blocks ? 0 : w.lo;
-    hi = i < w.sink_blocks ? w.sinks : w.end;
+    lo = !JOINT && i < w.sink_blocks ? 0 : w.lo;
+    hi = !JOINT && i < w.sink_blocks ? w.sinks : w.end;
 }
 
 // Sequence b as the tensor cores' pairs of tiles see it: its first token, its
@@ -274,6 +281,7 @@ __device__ __forceinline__ TcSeq tc_seq(const TcAttnParams& p, int b) {
 __device__ __forceinline__ int tc_seqs(const TcAttnParams& p) { return p.prefix ? 1 : p.a.kv.n_seqs; }
 
 // Pair `tile` of that sequence.
+template <bool JOINT>
 __device__ __forceinline__ void pair_work(const TcAttnParams& p, int b, const TcSeq& q, int tile, TcWork& w) {
     const KvView& kv = p.a.kv;
     const int pair = 2 * p.tile_tokens;
@@ -303,11 +311,18 @@ __device__ __forceinline__ void pair_work(const TcAttnParams& p, int b, const Tc
     w.sinks = int(sinks);
     w.sink_blocks = (w.sinks + kKeys - 1) / kKeys;
     w.blocks = w.sink_blocks + (w.end > w.lo ? (w.end + kKeys - 1) / kKeys - w.lo / kKeys : 0);
+    if (JOINT) {
+        const int page = 1 << kv.page_shift;
+        w.base = w.lo >= page ? (w.lo & ~(page - 1)) - page : 0;
+        w.sink_blocks = 0;
+        w.blocks = w.end > w.lo ? (w.end - w.base + kKeys - 1) / kKeys : 0;
+    }
 }
 
 // The tile pair with the given number, counted over all sequences (a sequence
 // of n tokens has ceil(n / pair)); false: there is none.  One warp finds it,
 // 32 sequences at a time.
+template <bool JOINT>
 __device__ __forceinline__ bool find_pair(const TcAttnParams& p, int number, int lane, TcWork& w) {
     const int pair = 2 * p.tile_tokens, seqs = tc_seqs(p);
     int base = 0;
@@ -332,7 +347,7 @@ __device__ __forceinline__ bool find_pair(const TcAttnParams& p, int number, int
         q.t0 = __shfl_sync(0xffffffffu, q.t0, src);
         q.tokens = __shfl_sync(0xffffffffu, q.tokens, src);
         q.len = __shfl_sync(0xffffffffu, q.len, src);
-        pair_work(p, b0 + src, q, number - before, w);
+        pair_work<JOINT>(p, b0 + src, q, number - before, w);
         return true;
     }
     return false;
@@ -345,12 +360,13 @@ __device__ __forceinline__ bool find_pair(const TcAttnParams& p, int number, int
 // without them the CTA whose range held the first pairs of a prompt, of a block
 // or two each, took twice as long as the others.  Places of one head of a
 // sequence, and the most blocks that a pair has:
+template <bool JOINT>
 __device__ __forceinline__ int seq_blocks(const TcAttnParams& p, int b, const TcSeq& q, int lane, int& most) {
     const int pair = 2 * p.tile_tokens, tiles = (q.tokens + pair - 1) / pair;
     int sum = 0;
     for (int i = lane; i < tiles; i += 32) {
         TcWork w;
-        pair_work(p, b, q, i, w);
+        pair_work<JOINT>(p, b, q, i, w);
         const int n = w.blocks > 0 ? w.blocks : 1;
         sum += kFixed + n;
         most = most > n ? most : n;
@@ -365,6 +381,7 @@ struct Range {
     TcWork w;
 };
 // The next pair that has tokens, from (b, tile) on; false: the line ends.
+template <bool JOINT>
 __device__ __forceinline__ bool range_pair(const TcAttnParams& p, Range& r) {
     const int pair = 2 * p.tile_tokens, seqs = tc_seqs(p);
     while (r.tile >= r.tiles) {
@@ -373,15 +390,16 @@ __device__ __forceinline__ bool range_pair(const TcAttnParams& p, Range& r) {
         r.tile = 0;
         r.tiles = (r.q.tokens + pair - 1) / pair;
     }
-    pair_work(p, r.b, r.q, r.tile, r.w);
+    pair_work<JOINT>(p, r.b, r.q, r.tile, r.w);
     return true;
 }
 // This CTA's range.
+template <bool JOINT>
 __device__ __forceinline__ void open_range(const TcAttnParams& p, int lane, Range& r) {
     const int seqs = tc_seqs(p), heads = p.a.kv.n_heads;
     int64_t U = 0;
     int most = 1;
-    for (int b = 0; b < seqs; ++b) U += int64_t(seq_blocks(p, b, tc_seq(p, b), lane, most)) * heads;
+    for (int b = 0; b < seqs; ++b) U += int64_t(seq_blocks<JOINT>(p, b, tc_seq(p, b), lane, most)) * heads;
     most = __reduce_max_sync(0xffffffffu, most);
     // a pair of n blocks lies in at most n / share + 2 ranges: its slots hold them
     r.share = (U + gridDim.x - 1) / gridDim.x;
@@ -394,13 +412,13 @@ __device__ __forceinline__ void open_range(const TcAttnParams& p, int lane, Rang
     r.begin = 0;
     for (r.b = 0;; ++r.b) {
         r.q = tc_seq(p, r.b);
-        const int64_t n = int64_t(seq_blocks(p, r.b, r.q, lane, most)) * heads;
+        const int64_t n = int64_t(seq_blocks<JOINT>(p, r.b, r.q, lane, most)) * heads;
         if (from < r.begin + n) break;
         r.begin += n;
     }
     r.tiles = (r.q.tokens + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
     for (r.tile = 0;; ++r.tile) {
-        pair_work(p, r.b, r.q, r.tile, r.w);
+        pair_work<JOINT>(p, r.b, r.q, r.tile, r.w);
         const int64_t n = int64_t(kFixed + (r.w.blocks > 0 ? r.w.blocks : 1)) * heads;
         if (from < r.begin + n) break;
         r.begin += n;
@@ -411,6 +429,7 @@ __device__ __forceinline__ void open_range(const TcAttnParams& p, int lane, Rang
     r.i = int(from - r.begin);
 }
 // The next piece of it that has blocks (or is a pair without any).
+template <bool JOINT>
 __device__ __forceinline__ bool take_range(const TcAttnParams& p, Range& r, TcWork& w) {
     while (r.left > 0) {
         const int units = kFixed + (r.w.blocks > 0 ? r.w.blocks : 1);
@@ -429,7 +448,7 @@ __device__ __forceinline__ bool take_range(const TcAttnParams& p, Range& r, TcWo
             r.i = 0;
             if (++r.w.hk == p.a.kv.n_heads) {
                 ++r.tile;
-                const bool some = range_pair(p, r);
+                const bool some = range_pair<JOINT>(p, r);
                 r.w.hk = 0;
                 if (!some) r.left = 0;
             }
@@ -439,10 +458,11 @@ __device__ __forceinline__ bool take_range(const TcAttnParams& p, Range& r, TcWo
     return false;
 }
 
+template <bool JOINT>
 __device__ __forceinline__ bool block_has_unseen(const TcWork& w, int i) {
     int lo, hi;
-    key_range(w, i, lo, hi);
-    const int j0 = key_block(w, i);
+    key_range<JOINT>(w, i, lo, hi);
+    const int j0 = key_block<JOINT>(w, i);
     return j0 < lo || j0 + kKeys > hi;
 }
 __device__ __forceinline__ int count_pairs(const TcAttnParams& p, int lane) {
@@ -470,7 +490,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitNs, err, code));
 }
 
-template <typename T, int DIM>
+template <typename T, int DIM, bool JOINT>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ TcAttnParams p) {
     using G = TcGeom<DIM>;
     constexpr int NS = G::kSlots;
@@ -568,8 +588,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 // lane x of the first `boxes` finds the page of its box of the block, one block ahead
                 const auto page_of_box = [&](int i) -> int {
                     int lo, hi;
-                    key_range(w, i, lo, hi);
-                    const int j = key_block(w, i) + lane * page_keys;
+                    key_range<JOINT>(w, i, lo, hi);
+                    if (JOINT && (i | lane) == 0) return page_of(kv, w.b, 0);
+                    const int j = key_block<JOINT>(w, i) + lane * page_keys;
                     return lane < boxes && j + page_keys > lo && j < hi ? page_of(kv, w.b, j) : -1;
                 };
                 int next_page = page_of_box(w.i0);
@@ -577,7 +598,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     const int page = next_page;
                     if (i + 1 < w.i0 + w.nb) next_page = page_of_box(i + 1);
                     const unsigned live = __ballot_sync(0xffffffffu, page >= 0);
-                    const int in_page = (key_block(w, i) + lane * page_keys) & ((1 << kv.page_shift) - 1);
+                    const int in_page = (key_block<JOINT>(w, i) + lane * page_keys) & ((1 << kv.page_shift) - 1);
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
                         if (issued >= NS && !(ok = warp_wait(&kv_empty[at.slot], at.phase ^ 1, kv.err, kErrTimeoutEmpty))) break;
@@ -607,13 +628,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             // work would sit on another.
             const int pairs = p.slots == 0 ? count_pairs(p, lane) : 0;
             Range r;
-            if (p.slots > 0) open_range(p, lane, r);
+            if (p.slots > 0) open_range<JOINT>(p, lane, r);
             for (int n = 0;; ++n) {
                 if (n >= 2 && !warp_wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, kv.err, kErrTimeoutEmpty)) break;
                 TcWork w;
                 bool more;
                 if (p.slots > 0) {
-                    more = take_range(p, r, w);
+                    more = take_range<JOINT>(p, r, w);
                 } else {
                     int item = int(blockIdx.x);
                     if (n > 0) {
@@ -623,7 +644,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     }
                     // the pairs with the most keys (the last of a sequence) first
                     const int number = item / kv.n_heads;
-                    more = number < pairs && find_pair(p, pairs - 1 - number, lane, w);
+                    more = number < pairs && find_pair<JOINT>(p, pairs - 1 - number, lane, w);
                     w.hk = item - number * kv.n_heads;
                     w.split = w.i0 = 0;
                     w.parts = 1;
@@ -747,13 +768,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
                         if (!(ok = warp_wait(&kv_full[at.slot], at.phase, kv.err, kErrTimeoutFull))) break;
-                        if (v && block_has_unseen(w, i)) {
+                        if (v && block_has_unseen<JOINT>(w, i)) {
                             int lo, hi;
-                            key_range(w, i, lo, hi);
-                            const int j0 = key_block(w, i);
+                            key_range<JOINT>(w, i, lo, hi);
+                            const int j0 = key_block<JOINT>(w, i), firsts = JOINT && i == 0 ? w.sinks : 0;
                             // (eight lanes a row of 128 bytes: no bank conflicts)
                             for (int r = lane >> 3; r < kKeys; r += 4)
-                                if (j0 + r < lo || j0 + r >= hi)
+                                if ((j0 + r < lo || j0 + r >= hi) && (!JOINT || r >= firsts))
 #pragma unroll
                                     for (int c = 0; c < G::kPanels; ++c)
                                         *reinterpret_cast<uint4*>(ring + at.slot * G::kTileBytes + c * G::kPanelBytes + r * 128 + 16 * (lane & 7)) =
@@ -817,16 +838,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 tc_after();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) ld32(sa + 32 * c, s + 32 * c);
-                const int j0 = key_block(w, w.i0 + i);
+                const int j0 = key_block<JOINT>(w, w.i0 + i);
                 int lo, hi;
-                key_range(w, w.i0 + i, lo, hi);
+                key_range<JOINT>(w, w.i0 + i, lo, hi);
                 // the row sees [first, last] (a thread without a row: whatever does not make its warp mask)
-                const int first = !live || w.i0 + i < w.sink_blocks ? 0 : (wlo > lo ? wlo : lo);
+                const int first = !live || (!JOINT && w.i0 + i < w.sink_blocks) ? 0 : (wlo > lo ? wlo : lo);
                 const int last = !live ? INT32_MAX - 1 : pos < hi - 1 ? pos : hi - 1;
                 wait_ld();
                 if (__any_sync(0xffffffffu, first > j0 || last < j0 + kKeys - 1)) {
-                    // and, in a window block, sinks that the pair's first row has in its window
-                    const int a = first - j0, b = last - j0, c0 = lo - j0, c1 = sinks - j0;
+                    // and, in a window block, sinks that the pair's first row has in its window (joint
+                    // sinks: all of them in the first block, whose first keys they are)
+                    const int a = first - j0, b = last - j0;
+                    const int c0 = JOINT ? 0 : lo - j0, c1 = !JOINT ? sinks - j0 : w.i0 + i == 0 ? sinks : 0;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t see = (bits_from(a - 32 * k) | (bits_from(c0 - 32 * k) & ~bits_from(c1 - 32 * k))) &
@@ -1027,15 +1050,21 @@ bool encode(CUtensorMap* m, bool f16, const void* ptr, int rank, const int64_t* 
 template <typename T, int DIM>
 cudaError_t launch_tc(const AttnParams& a, bool prefix, int slots, float* part_o, float* part_lse, unsigned* counter,
                       int sm_count, cudaStream_t s) {
-    static bool ready[64] = {false};
+    // Sinks in page 0, of several pages to a block: no block of their own.  (8191
+    // tokens, window 1024 + 4, pages of 64: 119 us, against 125 with one; a kernel of
+    // its own, since the same choice at run time made the other calls 1 to 3 % slower.)
+    const int page = 1 << a.kv.page_shift;
+    const bool joint = !prefix && a.window > 0 && a.sinks > 0 && a.sinks <= page && page < kKeys && a.shared_len == 0;
+    const auto kernel = joint ? attn_tc_kernel<T, DIM, true> : attn_tc_kernel<T, DIM, false>;
+    static bool ready[64][2] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!ready[dev]) {
-        e = cudaFuncSetAttribute(attn_tc_kernel<T, DIM>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(TcGeom<DIM>::kSmem));
+    if (!ready[dev][joint]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(TcGeom<DIM>::kSmem));
         if (e != cudaSuccess) return e;
-        ready[dev] = true;
+        ready[dev][joint] = true;
     }
     TcAttnParams p;
     memset(&p, 0, sizeof(p));
@@ -1054,7 +1083,7 @@ cudaError_t launch_tc(const AttnParams& a, bool prefix, int slots, float* part_o
     if (!encode_cache_maps(f16, a.kv, kKeys, &p.k_map, &p.v_map) || !encode(&p.q_map, f16, a.q, 3, qd, qs, qb))
         return cudaErrorInvalidValue;
     const int64_t items = tc_pairs(a.n_tokens, group, a.kv.n_seqs, prefix) * a.kv.n_heads;
-    return launch_serial(attn_tc_kernel<T, DIM>, dim3(unsigned(slots == 0 && items < sm_count ? items : sm_count)), kTcThreads,
+    return launch_serial(kernel, dim3(unsigned(slots == 0 && items < sm_count ? items : sm_count)), kTcThreads,
                          TcGeom<DIM>::kSmem, s, p);
 }
 

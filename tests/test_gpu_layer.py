@@ -177,6 +177,27 @@ def test_rising_scores(dim):
         b.check(out, lse, b.expect(sign), f"sign {sign}")
 
 
+@pytest.mark.parametrize("heads", [(32, 8, 128), (14, 2, 64)])
+@pytest.mark.parametrize("page,sinks", [(16, 16), (16, 1), (16, 17), (32, 5), (64, 64), (64, 3), (64, 65), (128, 7)])
+def test_first_keys_beside_a_window(heads, page, sinks):
+    """First keys that share the window's page, its block or neither, and pages
+    between them and the window that hold NaN and are given back."""
+    hq, hkv, dim = heads
+    for n, (q_lens, kv_lens, window) in enumerate([([150, 2], [700, 300], 90), ([200], [200], 70), ([130, 40], [131, 200], 1),
+                                                   ([140], [333], 150), ([129], [900], 640)]):
+        b = Batch(q_lens, kv_lens, hq, hkv, dim, page, (BF16, F16)[n % 2], seed=40 + n)
+        for s, (m, kv) in enumerate(zip(q_lens, kv_lens)):
+            first = max(0, kv - m + 1 - window)
+            for i in range(-(-kv // page)):
+                if page * i >= sinks and page * (i + 1) <= first:
+                    b.k[int(b.table_host[s, i])] = float("nan")
+                    b.v[int(b.table_host[s, i])] = float("nan")
+                    b.table[s, i] = -1
+        lse = torch.empty((b.T, hq), device="cuda")
+        out = qx.qx_attn_paged(b.kv, b.q, window=window, sinks=sinks, lse=lse)
+        b.check(out, lse, b.expect(dim ** -0.5, window, sinks), f"{heads} page {page} sinks {sinks} window {window} {q_lens}")
+
+
 @pytest.mark.parametrize("heads", [(32, 8, 128), (14, 2, 64), (2, 2, 80)])
 def test_pages_outside_the_window_may_be_given_back(heads):
     hq, hkv, dim = heads
