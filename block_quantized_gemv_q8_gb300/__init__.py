@@ -30,12 +30,13 @@ QX_CHAIN_MAX_ENTRIES = 4
 QX_F32, QX_F16, QX_BF16 = 0, 1, 30  # element types
 QX_MAX_HEAD_DIM = 256
 QX_MAX_GROUP = 128
+QX_ATTN_COUNTER_BYTES = 2304
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqx.so")
 
 EXPORTS = ["qx_quantize_act_q8", "qx_gemv", "qx_gemv_multi", "qx_gemm_prefill", "qx_gemm_prefill_ex",
            "qx_gemv_partials", "qx_gemv_chain", "qx_gemv_chain_noalloc", "qx_gemv_chain_scratch_bytes", "qx_row_bytes", "qx_repack",
-           "qx_rope_append", "qx_attn_paged", "qx_attn_shared", "qx_attn_scratch_bytes", "qx_block_norm",
+           "qx_rope_append", "qx_attn_paged", "qx_attn_shared", "qx_attn_scratch_bytes", "qx_block_norm", "qx_stream_capture_id",
            "qx_device_check", "qx_debug_timeout_probe", "qx_debug_mma_rate", "qx_debug_noalloc_fill",
            "qx_debug_trace_read", "qx_status_string", "qx_last_error", "qx_version"]
 
@@ -113,6 +114,8 @@ def lib() -> ctypes.CDLL:
         L.qx_attn_scratch_bytes.argtypes = [I64, I, I, I, I]
         L.qx_attn_scratch_bytes.restype = ctypes.c_size_t
         L.qx_block_norm.argtypes = [P, P]
+        L.qx_stream_capture_id.argtypes = [P]
+        L.qx_stream_capture_id.restype = ctypes.c_uint64
         L.qx_debug_mma_rate.argtypes = [I, ctypes.POINTER(ctypes.c_double), P]
         L.qx_debug_timeout_probe.argtypes = [ctypes.c_uint64, P]
         L.qx_debug_noalloc_fill.argtypes = [ctypes.c_uint32, P]
@@ -423,6 +426,56 @@ def _heads(t: torch.Tensor, shape: tuple, dtype, index: int, what: str) -> int:
     return a if shape[0] > 1 else shape[1] * shape[2]
 
 
+def _capture_of(stream, raw: int) -> int:
+    """The number of the capture that a call on `stream` (raw: its address) is part of; 0: none."""
+    if stream is None and not torch.cuda.is_current_stream_capturing():  # (0.1 us; the call below 0.5)
+        return 0
+    return lib().qx_stream_capture_id(raw)
+
+
+def _cleared(index: int, stream: int, nbytes: int):
+    """`nbytes` of GPU memory for attention calls on `stream`, their counters zeroed in the stream's order."""
+    device = torch.device("cuda", index)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device)):
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        buf[:QX_ATTN_COUNTER_BYTES].zero_()
+    return buf.data_ptr(), buf
+
+
+class _Scratch:
+    """The attention calls' scratch: a buffer for each stream, and buffers for captures.
+
+    A stream's buffer grows when a call needs more; the old one goes back to
+    the allocator, which reuses it in the stream's order.  A call under capture
+    never gets it: the graph would keep an address that is given back one day,
+    and its replays may run beside the stream's own calls.  Its buffer is part
+    of the graph's memory, like any tensor made under capture, and is cleared by
+    a node of the graph, so that each replay starts from zeroed counters; the
+    calls of one capture on one stream share it."""
+
+    def __init__(self, allocate=_cleared):
+        self._allocate = allocate  # (index, stream, bytes) -> address, owner
+        self._streams: dict = {}   # (index, stream) -> bytes, address, owner
+        self._captures: dict = {}  # capture -> the same for its streams
+
+    def get(self, index: int, stream: int, capture: int, need: int) -> int:
+        """Address of at least `need` bytes for a call on a stream, in capture `capture` (0: none)."""
+        if capture:
+            held = self._captures.get(capture)
+            if held is None:
+                held = {}
+                # Captures that are over need nothing of ours, and one that is
+                # not gets another cleared buffer.
+                self._captures = {capture: held}
+        else:
+            held = self._streams
+        have = held.get((index, stream))
+        if have is None or have[0] < need:
+            address, owner = self._allocate(index, stream, need)
+            have = held[index, stream] = (need, address, owner)
+        return have[1]
+
+
 class PagedKV:
     """A paged key/value cache and the batch that calls run on (``qx_kv``).
 
@@ -433,7 +486,8 @@ class PagedKV:
     caller's: the program updates the contents of table, kv_len and q_start in
     place from step to step (also between replays of a captured graph) and the
     calls read them on the GPU.  The object keeps them alive, and the attention
-    calls' scratch, one for each stream."""
+    calls' scratch, one for each stream; calls under capture take theirs from
+    the graph's own memory."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor,
                  q_start: torch.Tensor):
@@ -463,19 +517,18 @@ class PagedKV:
                       k.stride(0), k.stride(1), k.stride(2), table.data_ptr(), table.shape[1], kv_len.data_ptr(),
                       q_start.data_ptr(), n)
         self._ref = ctypes.byref(self._c)
-        self._scratch: dict = {}
+        self._scratch = _Scratch()
+        self._needs: dict = {}
 
-    def scratch(self, tokens: int, q_heads: int, stream: int) -> int:
-        """Address of the scratch of calls of at most these sizes on `stream` (grown when a call needs more)."""
-        have = self._scratch.get(stream)
-        if have is None or have[0] < tokens or have[1] < q_heads:
-            if have is not None:
-                tokens, q_heads = max(tokens, have[0]), max(q_heads, have[1])
-            need = int(lib().qx_attn_scratch_bytes(tokens, q_heads, self.heads, self.head_dim, self.n_seqs))
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device)):
-                buf = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.device)
-            have = self._scratch[stream] = (tokens, q_heads, buf, buf.data_ptr())
-        return have[3]
+    def scratch(self, tokens: int, q_heads: int, stream: int, capture: int = 0) -> int:
+        """Address of the scratch of a call of these sizes on `stream`, in capture `capture` (0: none)."""
+        need = self._needs.get((tokens, q_heads))
+        if need is None:
+            if len(self._needs) >= 256:
+                self._needs.clear()
+            need = max(256, int(lib().qx_attn_scratch_bytes(tokens, q_heads, self.heads, self.head_dim, self.n_seqs)))
+            self._needs[tokens, q_heads] = need
+        return self._scratch.get(self._index, stream, capture, need)
 
 
 def qx_rope_append(kv: PagedKV, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
@@ -554,7 +607,7 @@ def _attn(kv: PagedKV, q: torch.Tensor, scale, out, lse, stream):
         lp = _ptr(_need(lse, n * hq * 4, "lse"))
     s = _raw_stream(stream, index)
     return (kv._ref, q.data_ptr(), n, hq, q_stride, dim ** -0.5 if scale is None else scale), out, \
-        (out.data_ptr(), code, lp, kv.scratch(n, hq, s), s)
+        (out.data_ptr(), code, lp, kv.scratch(n, hq, s, _capture_of(stream, s)), s)
 
 
 def qx_attn_paged(kv: PagedKV, q: torch.Tensor, scale: float | None = None, window: int = 0, sinks: int = 0,

@@ -160,7 +160,8 @@ struct SplitGeom {
 // Scratch: arrival counters (one a worker, and 64 words for the tensor-core
 // kernel's; zero between calls), then two partial tiles a worker: o [16][DIM], then m and l of the 16 rows.
 constexpr int kMaxWorkers = 512;
-constexpr size_t kCounterBytes = (kMaxWorkers + 64) * 4;
+constexpr size_t kCounterBytes = QX_ATTN_COUNTER_BYTES;
+static_assert(kCounterBytes == (kMaxWorkers + 64) * 4, "the counters");
 template <int DIM>
 __host__ __device__ constexpr int partial_floats() { return kRows * DIM + 2 * kRows; }
 

@@ -157,6 +157,16 @@ size_t qx_attn_scratch_bytes(int64_t n_tokens, int n_q_heads, int n_heads, int h
     return attn_scratch_bytes(n_tokens, n_q_heads, n_heads, head_dim, n_seqs);
 }
 
+uint64_t qx_stream_capture_id(qx_stream_t s) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(s), &status, &id) != cudaSuccess) {
+        cudaGetLastError();  // (the legacy stream may not be asked while another one is captured)
+        return 0;
+    }
+    return status == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 qx_status qx_block_norm(const qx_norm_args* a, qx_stream_t s) {
     if (!a) return QX_ERR_ARG;
     const int eb = elem_bytes(a->dtype), rb = elem_bytes(a->res_dtype);

@@ -440,9 +440,12 @@ qx_status qx_rope_append(const qx_kv* kv, const qx_qkv* in, const float* cos, co
  * Slots of the cache that no token of its sequence sees have no effect,
  * whatever they hold (pages outside the window may be given back).
  * scratch: device, qx_attn_scratch_bytes() of the same sizes, 256-byte
- * aligned, zero-filled before its first use; a completed call leaves it fit
- * for the next.  Calls that may overlap need separate scratch.
+ * aligned, its first QX_ATTN_COUNTER_BYTES bytes zero-filled before its first
+ * use; a completed call leaves it fit for the next.  Calls that may overlap
+ * need separate scratch, and so do the calls of a captured graph, whose replays
+ * use it for as long as the graph lives.
  */
+#define QX_ATTN_COUNTER_BYTES 2304
 qx_status qx_attn_paged(const qx_kv* kv, const void* q, int64_t n_tokens, int n_q_heads, int64_t q_stride,
                         float scale, int64_t window, int64_t sinks, void* out, qx_dtype out_dtype, float* lse,
                         void* scratch, qx_stream_t s);
@@ -462,6 +465,11 @@ qx_status qx_attn_shared(const qx_kv* kv, const void* q, int64_t n_tokens, int n
 /* Device scratch bytes that qx_attn_paged and qx_attn_shared need on the
  * current device for at most these sizes; 0 for invalid ones. */
 size_t qx_attn_scratch_bytes(int64_t n_tokens, int n_q_heads, int n_heads, int head_dim, int n_seqs);
+
+/* The number of the capture that stream s takes part in, another one for each
+ * capture of the process; 0 outside of captures.  A program that keeps scratch
+ * for its streams learns by it when a call's has to be a graph's own. */
+uint64_t qx_stream_capture_id(qx_stream_t s);
 
 /*
  * The step from one block of a layer to the next, a row at a time:
