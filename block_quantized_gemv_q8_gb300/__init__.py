@@ -485,9 +485,13 @@ class PagedKV:
     kv_len: int32 [n_seqs]; q_start: int32 [n_seqs + 1].  The tensors are the
     caller's: the program updates the contents of table, kv_len and q_start in
     place from step to step (also between replays of a captured graph) and the
-    calls read them on the GPU.  The object keeps them alive, and the attention
-    calls' scratch, one for each stream; calls under capture take theirs from
-    the graph's own memory."""
+    calls read them on the GPU.  The object keeps them alive.  The attention
+    calls' scratch is shared by all caches, one for each stream; calls under
+    capture take theirs from the graph's own memory."""
+
+    # Calls on one stream run one after another, so the caches of a stack's
+    # layers share its buffer (32 query heads of 128, 265 tokens or more: 144 MB).
+    _scratch = _Scratch()
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor,
                  q_start: torch.Tensor):
@@ -517,7 +521,6 @@ class PagedKV:
                       k.stride(0), k.stride(1), k.stride(2), table.data_ptr(), table.shape[1], kv_len.data_ptr(),
                       q_start.data_ptr(), n)
         self._ref = ctypes.byref(self._c)
-        self._scratch = _Scratch()
         self._needs: dict = {}
 
     def scratch(self, tokens: int, q_heads: int, stream: int, capture: int = 0) -> int:

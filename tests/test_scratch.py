@@ -78,3 +78,21 @@ def test_captures_that_are_over_are_let_go(pool):
 def test_outside_of_captures_there_is_no_capture():
     qx.build_library()
     assert qx.lib().qx_stream_capture_id(ctypes.c_void_p(None)) == 0
+
+
+def test_the_caches_of_a_stack_share_a_streams_scratch(monkeypatch):
+    """Each object had one of its own: 144 MB for every layer of a stack."""
+    qx.build_library()
+    allocate = Allocator()
+    monkeypatch.setattr(qx.PagedKV, "_scratch", qx._Scratch(allocate))
+
+    def cache():
+        kv = object.__new__(qx.PagedKV)
+        kv.heads, kv.head_dim, kv.n_seqs, kv._index, kv._needs = 8, 128, 1, 0, {}
+        return kv
+
+    layers = [cache() for _ in range(4)]
+    assert len({kv.scratch(300, 32, 7) for kv in layers}) == 1
+    assert len({kv.scratch(1, 32, 7) for kv in layers}) == 1
+    assert len({kv.scratch(1, 32, 7, 5) for kv in layers}) == 1  # and a graph's
+    assert [m[:2] for m in allocate.made] == [(0, 7), (0, 7)] and allocate.made[1][2] < allocate.made[0][2]
