@@ -475,6 +475,10 @@ class _Scratch:
             have = held[index, stream] = (need, address, owner)
         return have[1]
 
+    def drop(self):
+        """Let all buffers go: calls that did not complete may have left their counters anywhere."""
+        self._streams, self._captures = {}, {}
+
 
 class PagedKV:
     """A paged key/value cache and the batch that calls run on (``qx_kv``).
@@ -733,8 +737,13 @@ def qx_debug_mma_rate(kind: int, stream=None) -> float:
 
 
 def qx_device_check(stream=None) -> int:
-    """Synchronise the stream and return (and clear) the device error status."""
-    return int(lib().qx_device_check(_stream(stream)))
+    """Synchronise the stream and return (and clear) the device error status.
+
+    After a wait that ran out the attention calls start from new scratch."""
+    st = int(lib().qx_device_check(_stream(stream)))
+    if st == QX_ERR_DEVICE_TIMEOUT:
+        PagedKV._scratch.drop()
+    return st
 
 
 def qx_debug_timeout_probe(limit_ns: int, stream=None):

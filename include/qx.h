@@ -441,9 +441,11 @@ qx_status qx_rope_append(const qx_kv* kv, const qx_qkv* in, const float* cos, co
  * whatever they hold (pages outside the window may be given back).
  * scratch: device, qx_attn_scratch_bytes() of the same sizes, 256-byte
  * aligned, its first QX_ATTN_COUNTER_BYTES bytes zero-filled before its first
- * use; a completed call leaves it fit for the next.  Calls that may overlap
- * need separate scratch, and so do the calls of a captured graph, whose replays
- * use it for as long as the graph lives.
+ * use; a completed call leaves it fit for the next.  After a bounded wait that
+ * ran out (QX_ERR_DEVICE_TIMEOUT from qx_device_check) they have to be
+ * zero-filled again.  Calls that may overlap need separate scratch, and so do
+ * the calls of a captured graph, whose replays use it for as long as the graph
+ * lives.
  */
 #define QX_ATTN_COUNTER_BYTES 2304
 qx_status qx_attn_paged(const qx_kv* kv, const void* q, int64_t n_tokens, int n_q_heads, int64_t q_stride,

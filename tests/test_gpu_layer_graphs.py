@@ -145,3 +145,20 @@ def test_shared_prefix_in_a_graph(shared, tails):
         g.replay()
         torch.cuda.synchronize()
         b.check(out, None, expected)
+
+
+def test_calls_after_a_wait_that_ran_out():
+    """They start from new scratch, and a captured graph clears its own."""
+    a, b = Call(Batch([1, 1], [3000, 900], 8, 2, 128, 16, BF16, seed=9)), Call(Batch([150], [2000], 8, 2, 128, 16, BF16, seed=10))
+    a(), b()
+    g = captured(lambda: (a(), b()))
+    # what calls that gave up could leave: counters that are not zero
+    scratch = a.kv._scratch
+    for _, _, buf in list(scratch._streams.values()) + [h for held in scratch._captures.values() for h in held.values()]:
+        buf[:qx.QX_ATTN_COUNTER_BYTES].view(torch.int32).fill_(3)
+    qx.qx_debug_timeout_probe(5_000_000)
+    assert qx.qx_device_check() == qx.QX_ERR_DEVICE_TIMEOUT
+    for run in (lambda: (a(), b()), g.replay, lambda: (a(), b())):
+        a.wrong(), b.wrong()
+        run()
+        a.check("a"), b.check("b")

@@ -96,3 +96,18 @@ def test_the_caches_of_a_stack_share_a_streams_scratch(monkeypatch):
     assert len({kv.scratch(1, 32, 7) for kv in layers}) == 1
     assert len({kv.scratch(1, 32, 7, 5) for kv in layers}) == 1  # and a graph's
     assert [m[:2] for m in allocate.made] == [(0, 7), (0, 7)] and allocate.made[1][2] < allocate.made[0][2]
+
+
+@pytest.mark.parametrize("status", [qx.QX_ERR_DEVICE_TIMEOUT, qx.QX_ERR_RANGE, qx.QX_OK])
+def test_scratch_of_calls_that_gave_up_is_not_used_again(monkeypatch, status):
+    """A wait that ran out leaves arrival counters that are not zero; a page out of range does not."""
+    class Lib:
+        qx_device_check = staticmethod(lambda stream: status)
+
+    allocate = Allocator()
+    monkeypatch.setattr(qx.PagedKV, "_scratch", qx._Scratch(allocate))
+    monkeypatch.setattr(qx, "lib", lambda: Lib)
+    old = [qx.PagedKV._scratch.get(0, 7, capture, 100) for capture in (0, 3)]
+    assert qx.qx_device_check(stream=0) == status
+    new = [qx.PagedKV._scratch.get(0, 7, capture, 100) for capture in (0, 3)]
+    assert set(old).isdisjoint(new) if status == qx.QX_ERR_DEVICE_TIMEOUT else old == new
