@@ -865,8 +865,9 @@ int slots_for(int64_t pairs, int64_t blocks, int seqs, int64_t rows, int64_t spa
 }  // namespace
 
 size_t attn_scratch_bytes(int64_t n_tokens, int n_q_heads, int, int head_dim, int) {
-    const int64_t rows = n_tokens * n_q_heads;
-    return kSplitScratch + (head_dim == 64 || head_dim == 128 ? size_t(part_rows(rows)) * (head_dim + 1) * 4 : 0);
+    // calls of up to this head size: only those of 64 and 128 leave parts
+    const int dim = head_dim < 64 ? 0 : head_dim < 128 ? 64 : 128;
+    return kSplitScratch + (dim > 0 ? size_t(part_rows(n_tokens * n_q_heads)) * (dim + 1) * 4 : 0);
 }
 
 cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaStream_t s) {

@@ -115,3 +115,16 @@ def test_block_norm_refusals(lib):
 
 def test_new_status_has_a_name(lib):
     assert qx.qx_status_string(qx.QX_ERR_RANGE).startswith("QX_ERR_RANGE")
+
+
+def test_scratch_sizes_serve_every_smaller_call(lib):
+    """A caller may size once for the largest of every argument."""
+    size, last = lib.qx_attn_scratch_bytes, 0
+    for dim in range(8, 257, 8):
+        assert size(300, 32, 8, dim, 4) >= last, dim
+        last = size(300, 32, 8, dim, 4)
+    for tokens in (0, 1, 2, 3, 263, 264, 265, 266, 4095, 4096, 4097, 100000):
+        for heads in (8, 16, 32, 64):
+            most = size(tokens, heads, 8, 128, 9)
+            assert all(size(t, h, hk, d, n) <= most for t in (0, tokens // 2, max(0, tokens - 1), tokens) for h in (8, heads)
+                       for hk in (1, 8) for d in (8, 64, 80, 128) for n in (1, 9)), (tokens, heads)
