@@ -45,6 +45,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     const int seq = seq_of_token(p.kv, t);
     if (seq < 0) return;
     const int64_t pos = position_of(p.kv, seq, t);
+    // a position without angles: nothing of the token is written, turned or not
+    if (p.rot > 0 && pos >= p.n_pos) {
+        atomicOr(p.kv.err, kErrRange);
+        return;
+    }
     D* dst;
     if (is_q) {
         dst = static_cast<D*>(p.q_out) + (int64_t(t) * p.n_q_heads + head) * dim;
@@ -58,10 +63,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 #pragma unroll
         for (int i = 0; i < 4; ++i) lo[i] = hi[i] = 0.0f;
     } else if (turns) {
-        if (pos >= p.n_pos) {
-            atomicOr(p.kv.err, kErrRange);
-            return;
-        }
         float cs[4], sn[4];
         load_f32<4>(p.cos + pos * half + 4 * c, cs);
         load_f32<4>(p.sin + pos * half + 4 * c, sn);

@@ -417,7 +417,9 @@ typedef struct {
  * (GGUF's two conventions):  a' = a c - b s,  b' = b c + a s.  Elements from
  * rot on pass.  The arithmetic is in f32, rounded once to the cache's type.
  * rot is a multiple of 8, at most head_dim; 0 (cos and sin may be NULL)
- * rotates nothing.  Padding tokens append nothing and get zeros in q_out.
+ * rotates nothing.  Padding tokens append nothing and get zeros in q_out; a
+ * token whose position has no row in cos and sin appends nothing, and its rows
+ * of q_out are left as they are (QX_ERR_RANGE from qx_device_check).
  * Two tokens of a call that share a slot race; a page may belong to several
  * sequences as long as none of the call's tokens falls into it.
  */

@@ -1,0 +1,43 @@
+"""GPU tests of what the operators between the weight products do at their
+edges: what is out of range, what is not a number, what a type can hardly hold."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_gemv_q8_gb300 as qx
+from . import layer_reference as ref
+from .test_gpu_layer import BF16, F16, F32, Batch, table_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    qx.build_library()
+    qx.lib()
+    assert qx.qx_device_check() == qx.QX_OK
+
+
+@pytest.mark.parametrize("dim,rot", [(64, 64), (64, 32), (80, 40), (128, 128)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("src", [F32, BF16])
+def test_a_position_beyond_the_rotation_is_not_written(dim, rot, interleaved, src):
+    """Neither the token's key and value nor its queries, rotated elements or others."""
+    b = Batch([1, 2, 1], [20, 34, 5], 4, 2, dim, 16, BF16)
+    x = torch.randn(4, 8, dim, device="cuda").to(src)
+    cos, sin = table_of(rot // 2, 33)  # position 33, sequence 1's last, has no row
+    q_out = torch.full((4, 4, dim), 3.0, dtype=BF16, device="cuda")
+    before = b.k.clone(), b.v.clone()
+    qx.qx_rope_append(b.kv, x[:, :4], x[:, 4:6], x[:, 6:], cos, sin, interleaved, q_out)
+    assert qx.qx_device_check() == qx.QX_ERR_RANGE
+    assert (q_out[2] == 3.0).all() and (q_out[[0, 1, 3]] != 3.0).any(-1).all()
+    for cache, was in zip((b.k, b.v), before):
+        same = cache.view(torch.int16) == was.view(torch.int16)
+        for seq, pos in ((0, 19), (1, 32), (2, 4)):
+            page, slot = int(b.table_host[seq, pos // 16]), pos % 16
+            assert not same[page, :, slot].all()
+            same[page, :, slot] = True
+        assert same.all(), "only the good tokens' slots may change"
+    # without a rotation the table does not matter
+    qx.qx_rope_append(b.kv, x[:, :4], x[:, 4:6], x[:, 6:], q_out=q_out)
+    assert qx.qx_device_check() == qx.QX_OK and torch.equal(q_out, x[:, :4].to(BF16))
