@@ -37,7 +37,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqx.so")
 EXPORTS = ["qx_quantize_act_q8", "qx_gemv", "qx_gemv_multi", "qx_gemm_prefill", "qx_gemm_prefill_ex",
            "qx_gemv_partials", "qx_gemv_chain", "qx_gemv_chain_noalloc", "qx_gemv_chain_scratch_bytes", "qx_row_bytes", "qx_repack",
            "qx_rope_append", "qx_attn_paged", "qx_attn_shared", "qx_attn_scratch_bytes", "qx_block_norm", "qx_stream_capture_id",
-           "qx_device_check", "qx_debug_timeout_probe", "qx_debug_mma_rate", "qx_debug_noalloc_fill",
+           "qx_device_check", "qx_debug_timeout_probe", "qx_debug_agree_probe", "qx_debug_mma_rate", "qx_debug_noalloc_fill",
            "qx_debug_trace_read", "qx_status_string", "qx_last_error", "qx_version"]
 
 
@@ -118,6 +118,7 @@ def lib() -> ctypes.CDLL:
         L.qx_stream_capture_id.restype = ctypes.c_uint64
         L.qx_debug_mma_rate.argtypes = [I, ctypes.POINTER(ctypes.c_double), P]
         L.qx_debug_timeout_probe.argtypes = [ctypes.c_uint64, P]
+        L.qx_debug_agree_probe.argtypes = [ctypes.c_uint64, P, P]
         L.qx_debug_noalloc_fill.argtypes = [ctypes.c_uint32, P]
         L.qx_debug_trace_read.argtypes = [P, ctypes.c_size_t]
         L.qx_status_string.argtypes = [I]
@@ -128,7 +129,7 @@ def lib() -> ctypes.CDLL:
         L.qx_version.restype = ctypes.c_char_p
         for n in ("qx_quantize_act_q8", "qx_gemv", "qx_gemv_multi", "qx_gemm_prefill", "qx_gemm_prefill_ex",
                   "qx_gemv_partials", "qx_gemv_chain", "qx_gemv_chain_noalloc",
-                  "qx_device_check", "qx_debug_timeout_probe",
+                  "qx_device_check", "qx_debug_timeout_probe", "qx_debug_agree_probe",
                   "qx_repack", "qx_rope_append", "qx_attn_paged", "qx_attn_shared", "qx_block_norm", "qx_debug_mma_rate", "qx_debug_noalloc_fill",
                   "qx_debug_trace_read"):
             getattr(L, n).restype = I
@@ -748,6 +749,11 @@ def qx_device_check(stream=None) -> int:
 
 def qx_debug_timeout_probe(limit_ns: int, stream=None):
     _check(lib().qx_debug_timeout_probe(limit_ns, _stream(stream)), "qx_debug_timeout_probe")
+
+
+def qx_debug_agree_probe(limit_ns: int, got: torch.Tensor, stream=None):
+    """Four waiting warps of which one gives up; got (int32 [4]): see qx_debug.h."""
+    _check(lib().qx_debug_agree_probe(limit_ns, _ptr(_need(got, 16, "got")), _stream(stream)), "qx_debug_agree_probe")
 
 
 def qx_debug_noalloc_fill(value: int, stream=None):

@@ -291,6 +291,17 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
     return a / b;
 }
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSplitWarps) : "memory"); }
+// The same, and whether every consumer came with `ok`: the answer is the same
+// for all, so they go on together or leave together.  (`ok` is warp-uniform.)
+__device__ __forceinline__ bool consumers_agree(bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(all)
+        : "r"(ok ? 1u : 0u), "n"(32 * kSplitWarps)
+        : "memory");
+    return all != 0;
+}
 
 // Four elements of row r of a tile (its sum o, not divided yet).
 template <typename T, int DIM>
@@ -615,9 +626,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
     const uint32_t k_row = ring + kr * 128, v_row = ring + G::kHalfStage + vr * 128;
     int slot = 0;
     uint32_t phase = 0;
-    bool ok = true;
-    // A wait that runs out ends the consumers: all four wait for the same copies
-    // and for the same time, so they end together, and none is left at a barrier.
+    // A wait that runs out ends the consumers, but not at the same time: each
+    // warp waits by itself, and copies may land between two warps' limits.  So
+    // the first barrier of a tile's end asks whether all four are there, and a
+    // warp that gave up comes to it once more (it is the next barrier of the
+    // others, whatever tile they are at: every worker's line ends with a tile's
+    // end).  All four leave there; none is left at a barrier.
+    bool ok = true, together = true;
     const auto arrived = [&]() {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], phase, kSplitWaitNs, p.kv.err, kErrTimeoutFull));
     };
@@ -751,7 +766,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                     *reinterpret_cast<float2*>(row + 8 * (d ^ (lane >> 2))) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
                 if ((lane & 3) == 0) *reinterpret_cast<float2*>(buf_ml + 2 * (8 * warp + (lane >> 2))) = make_float2(m[i], l[i]);
             }
-            consumers_sync();
+            if (i > 0) consumers_sync();
+            else if (!(together = consumers_agree(ok))) break;
             for (int x = threadIdx.x; x < live * (DIM / 4); x += 32 * kSplitWarps) {
                 const int r = x / (DIM / 4), d = x % (DIM / 4) * 4;
                 float2 ml[kSplitWarps];
@@ -778,6 +794,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                 }
             }
         }
+        if (!together) break;
         if (done.parts > 0) {
             // ---- this worker's part is written; the last to arrive joins all
             consumers_sync();
@@ -795,7 +812,31 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         }
         consumers_sync();  // the buffer is read
     }
+    if (!ok && together) consumers_agree(false);
     if (pp.beside) pdl_wait_prior_grid();  // complete only after that kernel, too
+}
+
+// Four consumers of which the first gives up on a unit after `limit_ns`, before
+// it arrives (half a limit later), and the others do not: who went on past the
+// barrier, by warp (test hook).
+__global__ void __launch_bounds__(32 * (kSplitWarps + 1)) agree_probe_kernel(uint64_t limit_ns, int* got, unsigned* err) {
+    __shared__ __align__(8) uint64_t full;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(&full, 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    if (warp == kSplitWarps) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < limit_ns + limit_ns / 2) {}
+        if (lane == 0) mbar_arrive(&full);
+        return;
+    }
+    const uint64_t limit = warp == 0 ? limit_ns : 100 * limit_ns;
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full, 0, limit, err, kErrTimeoutProbe));
+    const bool together = consumers_agree(ok);
+    if (lane == 0) got[warp] = (ok ? 1 : 0) | (together ? 2 : 0);
 }
 
 template <typename T, int DIM>
@@ -863,6 +904,11 @@ int slots_for(int64_t pairs, int64_t blocks, int seqs, int64_t rows, int64_t spa
 }
 
 }  // namespace
+
+cudaError_t launch_agree_probe(uint64_t limit_ns, int* got, unsigned* err, cudaStream_t s) {
+    agree_probe_kernel<<<1, 32 * (kSplitWarps + 1), 0, s>>>(limit_ns, got, err);
+    return cudaGetLastError();
+}
 
 size_t attn_scratch_bytes(int64_t n_tokens, int n_q_heads, int, int head_dim, int) {
     // calls of up to this head size: only those of 64 and 128 leave parts

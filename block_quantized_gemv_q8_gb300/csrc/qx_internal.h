@@ -256,6 +256,7 @@ struct NormParams {
 cudaError_t launch_rope(int src, int dst, const RopeParams& p, int sm_count, cudaStream_t s);
 cudaError_t launch_attn(int dtype, const AttnParams& p, int sm_count, cudaStream_t s);
 size_t attn_scratch_bytes(int64_t n_tokens, int n_q_heads, int n_heads, int head_dim, int n_seqs);
+cudaError_t launch_agree_probe(uint64_t limit_ns, int* got, unsigned* err, cudaStream_t s);
 cudaError_t launch_norm(int dtype, int res_dtype, const NormParams& p, bool vec, int sm_count, cudaStream_t s);
 
 }  // namespace qx

@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "../../include/qx.h"
+#include "../../include/qx_debug.h"
 #include "qx_internal.h"
 
 namespace qx {
@@ -211,6 +212,15 @@ qx_status qx_block_norm(const qx_norm_args* a, qx_stream_t s) {
                      on16(a->w_pre) && on16(a->r_out) && on16(a->x) && a->y_stride % 8 == 0 && a->r_stride % 8 == 0 &&
                      a->gate_stride % 8 == 0 && a->r_out_stride % 8 == 0 && a->x_stride % 8 == 0;
     return report_cuda(launch_norm(a->dtype, a->res_dtype, p, vec, sms, reinterpret_cast<cudaStream_t>(s)), "norm launch");
+}
+
+qx_status qx_debug_agree_probe(uint64_t limit_ns, int32_t* got, qx_stream_t s) {
+    if (!got || limit_ns < 1000000ull || limit_ns > 100000000ull) return QX_ERR_ARG;
+    int sms = 0;
+    unsigned* err = nullptr;
+    const qx_status st = current_device(&sms, &err);
+    if (st != QX_OK) return st;
+    return report_cuda(launch_agree_probe(limit_ns, got, err, reinterpret_cast<cudaStream_t>(s)), "probe launch");
 }
 
 }  // extern "C"

@@ -19,6 +19,14 @@ extern "C" {
  * QX_ERR_DEVICE_TIMEOUT.  QX_ERR_ARG for a limit outside that range. */
 qx_status qx_debug_timeout_probe(uint64_t limit_ns, qx_stream_t s);
 
+/* Launch one CTA whose four warps wait for the same unit as the consumers of
+ * the split attention do, the first of them too short: it gives up after
+ * `limit_ns` (1 ms .. 100 ms), the unit comes half as much later, and all four
+ * meet.  got (device, 4 words): bit 0, the warp's unit came; bit 1, all came
+ * and the warps go on.  qx_device_check() then returns QX_ERR_DEVICE_TIMEOUT.
+ * QX_ERR_ARG for a null pointer or another limit. */
+qx_status qx_debug_agree_probe(uint64_t limit_ns, int32_t* got, qx_stream_t s);
+
 /* The device's warp-level tensor-core rate, multiply-adds x 2 per second, of
  * mma.sync int8 m16n8k32 (kind 0) or f16 m16n8k16 with an f32 accumulator
  * (kind 1), run from registers by every SM; sm_103a has no int8 tcgen05 MMA,

@@ -41,3 +41,13 @@ def test_a_position_beyond_the_rotation_is_not_written(dim, rot, interleaved, sr
     # without a rotation the table does not matter
     qx.qx_rope_append(b.kv, x[:, :4], x[:, 4:6], x[:, 6:], q_out=q_out)
     assert qx.qx_device_check() == qx.QX_OK and torch.equal(q_out, x[:, :4].to(BF16))
+
+
+@pytest.mark.parametrize("limit_ns", [1_000_000, 20_000_000])
+def test_a_warp_that_gives_up_takes_the_others_along(limit_ns):
+    """Its unit comes before the others' limit: they have it, and leave with the one that has not."""
+    got = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+    qx.qx_debug_agree_probe(limit_ns, got)
+    assert qx.qx_device_check() == qx.QX_ERR_DEVICE_TIMEOUT
+    assert got.tolist() == [0, 1, 1, 1]
+    assert qx.qx_device_check() == qx.QX_OK

@@ -128,3 +128,9 @@ def test_scratch_sizes_serve_every_smaller_call(lib):
             most = size(tokens, heads, 8, 128, 9)
             assert all(size(t, h, hk, d, n) <= most for t in (0, tokens // 2, max(0, tokens - 1), tokens) for h in (8, heads)
                        for hk in (1, 8) for d in (8, 64, 80, 128) for n in (1, 9)), (tokens, heads)
+
+
+def test_agree_probe_refusals(lib):
+    P = ctypes.c_void_p
+    for limit, got in ((10, A16), (1 << 40, A16), (1_000_000, None)):
+        assert lib.qx_debug_agree_probe(limit, P(got), None) == qx.QX_ERR_ARG
