@@ -407,6 +407,9 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
 def _raw_stream(stream, index: int) -> int:
     if stream is None:
         return _current_raw_stream(index)
@@ -425,13 +428,6 @@ def _heads(t: torch.Tensor, shape: tuple, dtype, index: int, what: str) -> int:
     if (c != 1 and shape[2] > 1) or (b != shape[2] and shape[1] > 1):
         raise ValueError(f"{what}: a token's heads must lie one after another (strides {(a, b, c)})")
     return a if shape[0] > 1 else shape[1] * shape[2]
-
-
-def _capture_of(stream, raw: int) -> int:
-    """The number of the capture that a call on `stream` (raw: its address) is part of; 0: none."""
-    if stream is None and not torch.cuda.is_current_stream_capturing():  # (0.1 us; the call below 0.5)
-        return 0
-    return lib().qx_stream_capture_id(raw)
 
 
 def _cleared(index: int, stream: int, nbytes: int):
@@ -531,6 +527,10 @@ class PagedKV:
     def scratch(self, tokens: int, q_heads: int, stream: int, capture: int = 0) -> int:
         """Address of the scratch of a call of these sizes on `stream`, in capture `capture` (0: none)."""
         need = self._needs.get((tokens, q_heads))
+        if need is not None and not capture:  # (the common case in line)
+            have = self._scratch._streams.get((self._index, stream))
+            if have is not None and have[0] >= need:
+                return have[1]
         if need is None:
             if len(self._needs) >= 256:
                 self._needs.clear()
@@ -614,8 +614,10 @@ def _attn(kv: PagedKV, q: torch.Tensor, scale, out, lse, stream):
             raise TypeError("lse is float32")
         lp = _ptr(_need(lse, n * hq * 4, "lse"))
     s = _raw_stream(stream, index)
+    # (the question about the current stream takes 0.1 us, the other one 0.5)
+    capture = 0 if stream is None and not _capturing() else lib().qx_stream_capture_id(s)
     return (kv._ref, q.data_ptr(), n, hq, q_stride, dim ** -0.5 if scale is None else scale), out, \
-        (out.data_ptr(), code, lp, kv.scratch(n, hq, s, _capture_of(stream, s)), s)
+        (out.data_ptr(), code, lp, kv.scratch(n, hq, s, capture), s)
 
 
 def qx_attn_paged(kv: PagedKV, q: torch.Tensor, scale: float | None = None, window: int = 0, sinks: int = 0,
