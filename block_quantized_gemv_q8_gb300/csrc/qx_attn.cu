@@ -6,6 +6,8 @@
 // turns (m, l, o) into (M, l e^(m-M) + sum e^(s_j-M), o e^(m-M) + ...), M =
 // max(m, m'); the output is o / l.  Exponents are taken to base 2 with
 // scale * log2(e) folded into the scores.
+#include <cfloat>
+
 #include "qx_attn.cuh"
 #include "qx_layer.cuh"
 
@@ -22,7 +24,7 @@ constexpr int kMaxDim = QX_MAX_HEAD_DIM;
 // 128) and reads a key once for every row: 64 tokens over windows of 4096 keys
 // take it 1.91 ms, where the split kernel takes 0.15.
 template <typename T>
-__global__ void __launch_bounds__(32 * kRowWarps) attn_row_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(32 * kRowWarps, 8) attn_row_kernel(const __grid_constant__ AttnParams p) {
     __shared__ float q[kMaxDim];
     __shared__ float om[kRowWarps], ol[kRowWarps], oo[kRowWarps][kMaxDim];
     pdl_wait_prior_grid();
@@ -37,7 +39,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_row_kernel(const __grid_c
     __syncthreads();
     const int64_t lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;  // first key of the window
     const int64_t sinks = p.sinks < lo ? p.sinks : lo;
-    float m = -INFINITY, l = 0.0f, o[kMaxDim / 32];
+    // The maximum begins at a number, so that no difference is inf - inf: fmaxf
+    // passes over scores that are no numbers, and those have to get into the sums.
+    float m = -FLT_MAX, l = 0.0f, o[kMaxDim / 32];
 #pragma unroll
     for (int i = 0; i < kMaxDim / 32; ++i) o[i] = 0.0f;
     const int64_t n = pos < 0 ? 0 : sinks + (pos + 1 - lo);  // keys seen: 0 .. sinks - 1, lo .. pos
@@ -65,7 +69,6 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_row_kernel(const __grid_c
 #pragma unroll
         for (int w = 16; w >= 1; w >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
         const float mn = fmaxf(m, mb);
-        if (mn == -INFINITY) continue;
         const float a = exp2f(m - mn), pr = exp2f(s - mn);
         l = l * a + pr;
         m = mn;
@@ -88,10 +91,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_row_kernel(const __grid_c
     for (int e = 0; e < kMaxDim / 32; ++e)
         if (lane + 32 * e < dim) oo[warp][lane + 32 * e] = o[e];
     __syncthreads();
-    float M = -INFINITY, L = 0.0f, a[kRowWarps];
+    float M = -FLT_MAX, L = 0.0f, a[kRowWarps];
     for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, om[w]);
     for (int w = 0; w < kRowWarps; ++w) {
-        a[w] = om[w] == -INFINITY ? 0.0f : exp2f(om[w] - M);
+        a[w] = exp2f(om[w] - M);
         L += a[w] * ol[w];
     }
     const int64_t row = int64_t(t) * p.n_q_heads + h;
@@ -322,6 +325,14 @@ __device__ __forceinline__ void write_four(const SplitParams& pp, const UnitInfo
     if (p.lse && d == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
+// (M, L) and (m, l) become one maximum and one sum.  Sums over scores that are
+// no numbers have a maximum of -inf, and stay what they are.
+__device__ __forceinline__ void join_sums(float& M, float& L, float m, float l) {
+    const float mn = fmaxf(M, m), base = mn == -INFINITY ? 0.0f : mn;
+    L = L * exp2_approx(M - base) + l * exp2_approx(m - base);
+    M = mn;
+}
+
 // The parts of a tile that several workers shared, joined by the consumers of
 // the last of them to arrive.
 template <typename T, int DIM>
@@ -343,18 +354,14 @@ __device__ __forceinline__ void join_parts(const SplitParams& pp, const UnitInfo
 #pragma unroll 4
         for (int i = i8; i < parts; i += 8) {
             const float2 ml = __ldcg(reinterpret_cast<const float2*>(src(i) + kRows * DIM + 2 * r8));
-            const float mn = fmaxf(M, ml.x);
-            if (mn != -INFINITY) L = L * exp2_approx(M - mn) + ml.y * exp2_approx(ml.x - mn);
-            M = mn;
+            join_sums(M, L, ml.x, ml.y);
             if (fits) weight[r8 * parts + i] = ml.x;
         }
     }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
         const float om = __shfl_xor_sync(0xffffffffu, M, o), ol = __shfl_xor_sync(0xffffffffu, L, o);
-        const float mn = fmaxf(M, om);
-        if (mn != -INFINITY) L = L * exp2_approx(M - mn) + ol * exp2_approx(om - mn);
-        M = mn;
+        join_sums(M, L, om, ol);
     }
     if (r8 < live) {
         if (fits)

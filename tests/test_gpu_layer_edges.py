@@ -51,3 +51,49 @@ def test_a_warp_that_gives_up_takes_the_others_along(limit_ns):
     assert qx.qx_device_check() == qx.QX_ERR_DEVICE_TIMEOUT
     assert got.tolist() == [0, 1, 1, 1]
     assert qx.qx_device_check() == qx.QX_OK
+
+
+def not_numbers(b, out, lse, rows):
+    """Rows `rows` (of [tokens, heads]) are not a number, their log-sum-exp neither; the others are right."""
+    assert qx.qx_device_check() == qx.QX_OK
+    o, l, mass, top = b.expect(b.dim ** -0.5)
+    got, gl = ref.f64(out), ref.f64(lse)
+    assert np.isnan(got[rows]).all() and np.isnan(gl[rows]).all()
+    good = ~rows
+    assert (np.abs(got - o) <= ref.attention_bound(o, mass, top, b.dim, b.dtype, out.dtype))[good].all()
+    assert (np.abs(gl - l) <= ref.lse_bound(l, top, b.dim))[good].all()
+
+
+NAN_BATCHES = [([1], [1]), ([1], [7000]), ([1, 1], [20, 700]), ([3, 2], [50, 3000]), ([140, 1], [140, 90]), ([130], [4000])]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 80])
+@pytest.mark.parametrize("q_lens,kv_lens", NAN_BATCHES)
+def test_a_query_that_is_not_a_number(dim, q_lens, kv_lens):
+    b = Batch(q_lens, kv_lens, 4, 2, dim, 16, BF16, seed=1)
+    rows = np.zeros((b.T, 4), dtype=bool)
+    rows[-1, 1] = rows[0, 2] = True
+    lse = torch.empty((b.T, 4), device="cuda")
+    clean = b.q.clone()
+    b.q[torch.from_numpy(rows).cuda()] = float("nan")
+    out = qx.qx_attn_paged(b.kv, b.q, lse=lse)
+    b.q.copy_(clean)
+    not_numbers(b, out, lse, rows)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 80])
+@pytest.mark.parametrize("q_lens,kv_lens", NAN_BATCHES)
+@pytest.mark.parametrize("which", ["one", "all"])
+def test_keys_that_are_not_numbers(dim, q_lens, kv_lens, which):
+    """One of the first sequence's keys, or all of them, of one key head."""
+    b = Batch(q_lens, kv_lens, 4, 2, dim, 16, F16, seed=2)
+    clean = b.k.clone()
+    last = kv_lens[0] - q_lens[0]  # the position of its first token: every token sees the keys up to it
+    for j in (range(last + 1) if which == "all" else [last]):
+        b.k[int(b.table_host[0, j // 16]), 1, j % 16] = float("nan")
+    rows = np.zeros((b.T, 4), dtype=bool)
+    rows[:q_lens[0], 2:] = True
+    lse = torch.empty((b.T, 4), device="cuda")
+    out = qx.qx_attn_paged(b.kv, b.q, lse=lse)
+    b.k.copy_(clean)
+    not_numbers(b, out, lse, rows)
