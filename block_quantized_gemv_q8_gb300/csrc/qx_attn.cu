@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                     o[d][2] *= a[1], o[d][3] *= a[1];
                 }
             }
-            const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+            const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0] - kLift<T, 0>, m[1] == -INFINITY ? 0.0f : m[1] - kLift<T, 0>};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
 #pragma unroll
                 for (int d = 0; d < DIM / 8; ++d)
                     *reinterpret_cast<float2*>(row + 8 * (d ^ (lane >> 2))) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
-                if ((lane & 3) == 0) *reinterpret_cast<float2*>(buf_ml + 2 * (8 * warp + (lane >> 2))) = make_float2(m[i], l[i]);
+                if ((lane & 3) == 0) *reinterpret_cast<float2*>(buf_ml + 2 * (8 * warp + (lane >> 2))) = make_float2(m[i] - kLift<T, 0>, l[i]);
             }
             if (i > 0) consumers_sync();
             else if (!(together = consumers_agree(ok))) break;

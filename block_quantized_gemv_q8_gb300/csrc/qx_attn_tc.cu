@@ -13,9 +13,10 @@
 //
 // O is rescaled by the warp that owns its rows, and only when a row's maximum
 // rose by more than kRescale powers of two: until then the old maximum stays
-// the base, P at most 2^kRescale, which both 16-bit types and the f32 sums
-// hold without loss.  The maximum, the sum of the unrounded exponentials and O
-// are f32.
+// the base, P at most 2^kRescale times what it would be, which bf16 and the f32
+// sums hold without loss; for f16 P is raised as far as the type goes, and the
+// maximum follows sooner.  The maximum, the sum of the unrounded exponentials
+// and O are f32.
 //
 // A block of 128 keys takes the pipe 2048 cycles for both tiles (head size 128)
 // and an SM's exponential units 1024; a tile's own chain -- scores 512 cycles,
@@ -62,7 +63,10 @@ constexpr int kSoftmaxWarps = 8;       // two warpgroups
 constexpr int kTcThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "registers the CTA was launched with");
-constexpr float kRescale = 8.0f;
+// (f16: 2 leaves room to raise P by 2^13.  Five chunks of prompts in f16: 63.8 us,
+// 62.4 with 8 and no room.)
+template <typename T>
+constexpr int kRescale = IsBf16<T>::value ? 8 : 2;
 constexpr int kFixed = 3;              // blocks that a pair's fixed cost (some 5 us) is worth
 constexpr int kMinPart = 8;            // blocks of a range at least: a part costs some 5 us beside them
 constexpr float kWritten = INFINITY;   // as a row's first base-2 log: the row is in the output already
@@ -865,7 +869,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 #pragma unroll
                     for (int y = 0; y < 4; ++y) mx[y] = x + 4 < kKeys ? max3(mx[y], s[x + y], s[x + 4 + y]) : fmaxf(mx[y], s[x + y]);
                 const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * f;
-                if (__any_sync(0xffffffffu, top > m + kRescale)) {
+                if (__any_sync(0xffffffffu, top > m + float(kRescale<T>))) {
                     const float mn = fmaxf(m, top);
                     const float a = mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
                     l *= a;
@@ -885,7 +889,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         }
                     }
                 }
-                const float base = m == -INFINITY ? 0.0f : m;
+                const float base = m == -INFINITY ? 0.0f : m - kLift<T, kRescale<T>>;
                 const uint64_t f2 = f32x2_pack(f, f), b2 = f32x2_pack(-base, -base);
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
@@ -921,7 +925,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             const bool to_part = p.part_o && (p.prefix || p.tails || w.parts > 1);
             const int64_t row = int64_t(w.t0 + tok) * p.a.n_q_heads + w.hk * group + head;
             const int64_t part = int64_t(split) * p.a.n_tokens * p.a.n_q_heads + row;
-            const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+            const float lse2 = l == 0.0f ? -INFINITY : m - kLift<T, kRescale<T>> + log2f(l);
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             if (live && p.part_o) {
                 p.part_lse[part] = to_part ? lse2 : kWritten;

@@ -436,9 +436,11 @@ qx_status qx_rope_append(const qx_kv* kv, const qx_qkv* in, const float* cos, co
  * one after another); out: [n_tokens, n_q_heads, head_dim], the cache's type
  * or QX_F32; lse (may be NULL): f32 [n_tokens, n_q_heads], the natural log of
  * sum_j p_j.  A row that sees no key (a padding token) gets zeros and -inf.
- * Scores, maxima, sums and outputs are held in f32; the probabilities are
- * rounded to the cache's type before they meet v (relative 2^-8 for bf16,
- * 2^-11 for f16, at most), so an f32 out carries that much too.
+ * Scores, maxima, sums and outputs are held in f32.  At head sizes 64 and 128
+ * the probabilities are rounded to the cache's type before they meet v, so an
+ * f32 out carries that much too: relative 2^-8 for bf16 and 2^-11 for f16, at
+ * most; f16 holds those below 2^-27 of the row's largest to 2^-38 of it.  At
+ * other head sizes they stay in f32.
  * Slots of the cache that no token of its sequence sees have no effect,
  * whatever they hold (pages outside the window may be given back).
  * scratch: device, qx_attn_scratch_bytes() of the same sizes, 256-byte

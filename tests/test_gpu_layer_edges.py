@@ -97,3 +97,27 @@ def test_keys_that_are_not_numbers(dim, q_lens, kv_lens, which):
     out = qx.qx_attn_paged(b.kv, b.q, lse=lse)
     b.k.copy_(clean)
     not_numbers(b, out, lse, rows)
+
+
+@pytest.mark.parametrize("q_lens", [[1], [3], [130]])
+@pytest.mark.parametrize("dim", [64, 128, 32])
+@pytest.mark.parametrize("nats", [12.75, 17.6])
+def test_unlikely_keys_beside_likely_ones_in_f16(q_lens, dim, nats):
+    """Every sixteenth key is a likely one whose value is zero: the output is what
+    f16 holds of the others' probabilities, 2^-18.4 or 2^-25.4 of the largest."""
+    n = 20000
+    b = Batch(q_lens, [n], 4, 2, dim, 64, F16, seed=7)
+    b.q.zero_()
+    b.q[..., 0] = 8.0
+    keys, values = np.zeros((n, 2, dim)), 1000.0 * (b.values[0] + 0.5)
+    keys[::16, :, 0], values[::16] = nats, 0.0
+    for i in range(-(-n // 64)):
+        m, page = min(64, n - 64 * i), int(b.table_host[0, i])
+        for cache, host in ((b.k, keys), (b.v, values)):
+            cache[page, :, :m] = torch.from_numpy(host[64 * i:64 * i + m]).to(F16).transpose(0, 1).cuda()
+    b.keys[0], b.values[0] = (ref.f64(torch.from_numpy(x).to(F16)) for x in (keys, values))
+    for out_dtype in (F16, F32):
+        lse = torch.empty((b.T, 4), device="cuda")
+        out = torch.empty((b.T, 4, dim), dtype=out_dtype, device="cuda")
+        qx.qx_attn_paged(b.kv, b.q, scale=0.125, out=out, lse=lse)
+        b.check(out, lse, b.expect(0.125), f"{q_lens} {dim} {nats} {out_dtype}")
