@@ -177,6 +177,12 @@ qx_status qx_block_norm(const qx_norm_args* a, qx_stream_t s) {
         !stride_ok(a->r_out_stride) || !stride_ok(a->x_stride))
         return QX_ERR_SHAPE;
     if (a->rows == 0) return QX_OK;
+    if (a->rows > 1) {
+        // rows written over one another would race, in place over other rows' inputs too
+        if ((a->r_out && a->r_out_stride < a->cols) || (a->x && a->x_stride < a->cols)) return QX_ERR_SHAPE;
+        if ((a->r_out && a->r_out == a->r && a->r_out_stride != a->r_stride) || (a->x && a->x == a->y && a->x_stride != a->y_stride))
+            return QX_ERR_SHAPE;
+    }
     if (!a->r) return QX_ERR_ARG;
     if ((a->w_pre != nullptr) != (a->x != nullptr) || (!a->r_out && !a->x)) return QX_ERR_ARG;
     if (!a->y && (a->gate || a->w_post)) return QX_ERR_ARG;

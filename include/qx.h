@@ -486,7 +486,9 @@ uint64_t qx_stream_capture_id(qx_stream_t s);
  * QX_BF16); w_post and w_pre: f32 [cols].  Rows lie y_stride, gate_stride, ...
  * elements apart (gate_stride 0: one gate for all rows).  y NULL: u = 0, so x
  * is the norm of r.  r_out NULL: r' is not written.  The arithmetic is in f32;
- * x comes from r' before it is rounded.  r_out may be r and x may be y.
+ * x comes from r' before it is rounded.  r_out may be r and x may be y, with
+ * the same stride; rows of r_out and of x may not overlap (strides of cols at
+ * least, where there are several rows).
  * 1 <= cols <= QX_MAX_COLS.
  */
 typedef struct {

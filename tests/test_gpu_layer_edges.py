@@ -121,3 +121,20 @@ def test_unlikely_keys_beside_likely_ones_in_f16(q_lens, dim, nats):
         out = torch.empty((b.T, 4, dim), dtype=out_dtype, device="cuda")
         qx.qx_attn_paged(b.kv, b.q, scale=0.125, out=out, lse=lse)
         b.check(out, lse, b.expect(0.125), f"{q_lens} {dim} {nats} {out_dtype}")
+
+
+def test_block_norm_refuses_output_rows_that_overlap():
+    y, r, w = torch.randn(4, 64, device="cuda"), torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    one, close = torch.empty(64, device="cuda").expand(4, 64), torch.empty(256, device="cuda").as_strided((4, 64), (56, 1))
+    wide = torch.randn(4, 128, device="cuda")
+    for bad in (dict(r_out=one), dict(r_out=close), dict(w_pre=w, x_out=one), dict(w_pre=w, x_out=close)):
+        with pytest.raises(qx.QxError) as e:
+            qx.qx_block_norm(y, r, **bad)
+        assert e.value.status == qx.QX_ERR_SHAPE
+    with pytest.raises(qx.QxError):  # in place, but in rows that lie otherwise
+        qx.qx_block_norm(y, wide[:, :64], r_out=wide.view(-1)[:256].view(4, 64))
+    # one row for all as an input, one row of any stride as an output
+    r2, _ = qx.qx_block_norm(y, r[:1].expand(4, 64))
+    assert torch.equal(r2, r[:1] + y)
+    r2, _ = qx.qx_block_norm(y[:1], r[:1], r_out=torch.empty(64, device="cuda").as_strided((1, 64), (0, 1)))
+    assert torch.equal(r2, r[:1] + y[:1]) and qx.qx_device_check() == qx.QX_OK

@@ -134,3 +134,17 @@ def test_agree_probe_refusals(lib):
     P = ctypes.c_void_p
     for limit, got in ((10, A16), (1 << 40, A16), (1_000_000, None)):
         assert lib.qx_debug_agree_probe(limit, P(got), None) == qx.QX_ERR_ARG
+
+
+def test_block_norm_refuses_output_rows_that_overlap(lib):
+    def call(**change):
+        a = dict(rows=2, cols=64, dtype=qx.QX_BF16, res_dtype=qx.QX_F32, y=A16, r=2 * A16, w_pre=A16, alpha=1.0, eps=1e-5, r_out=3 * A16,
+                 x=4 * A16, y_stride=64, r_stride=64, r_out_stride=64, x_stride=64)
+        a.update(change)
+        return lib.qx_block_norm(ctypes.byref(qx._Norm(**a)), None)
+
+    for bad in (dict(r_out_stride=0), dict(r_out_stride=63), dict(x_stride=0), dict(x_stride=56), dict(r_out=None, x_stride=8)):
+        assert call(**bad) == qx.QX_ERR_SHAPE, bad
+    # in place, each row over its own
+    for bad in (dict(r_out=2 * A16, r_stride=128), dict(r_out=2 * A16, r_out_stride=72), dict(x=A16, y_stride=0), dict(x=A16, y_stride=72)):
+        assert call(**bad) == qx.QX_ERR_SHAPE, bad
