@@ -6,8 +6,6 @@
 // turns (m, l, o) into (M, l e^(m-M) + sum e^(s_j-M), o e^(m-M) + ...), M =
 // max(m, m'); the output is o / l.  Exponents are taken to base 2 with
 // scale * log2(e) folded into the scores.
-#include <cfloat>
-
 #include "qx_attn.cuh"
 #include "qx_layer.cuh"
 
@@ -22,7 +20,8 @@ constexpr int kMaxDim = QX_MAX_HEAD_DIM;
 // (a lane scores a key, then owns every 32nd output element), joined at the
 // end.  It serves the head sizes that the kernels below do not (all but 64 and
 // 128) and reads a key once for every row: 64 tokens over windows of 4096 keys
-// take it 1.91 ms, where the split kernel takes 0.15.
+// take it 1.91 ms, where the split kernel takes 0.15.  (8 tokens over 2000 keys,
+// head size 80: 301 us; with the values' loads past a branch 400.)
 template <typename T>
 __global__ void __launch_bounds__(32 * kRowWarps, 8) attn_row_kernel(const __grid_constant__ AttnParams p) {
     __shared__ float q[kMaxDim];
@@ -37,59 +36,19 @@ __global__ void __launch_bounds__(32 * kRowWarps, 8) attn_row_kernel(const __gri
     const T* qr = static_cast<const T*>(p.q) + t * p.q_stride + int64_t(h) * dim;
     for (int d = threadIdx.x; d < dim; d += 32 * kRowWarps) q[d] = to_f32(qr[d]);
     __syncthreads();
-    const int64_t lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;  // first key of the window
-    const int64_t sinks = p.sinks < lo ? p.sinks : lo;
-    // The maximum begins at a number, so that no difference is inf - inf: fmaxf
-    // passes over scores that are no numbers, and those have to get into the sums.
-    float m = -FLT_MAX, l = 0.0f, o[kMaxDim / 32];
+    RowSums<kMaxDim / 32> r;
+    row_sums<T, 4>(p, seq, pos, hk, 0, INT64_MAX, 32 * warp, 32 * kRowWarps,
+                [&](int d, float (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < kMaxDim / 32; ++i) o[i] = 0.0f;
-    const int64_t n = pos < 0 ? 0 : sinks + (pos + 1 - lo);  // keys seen: 0 .. sinks - 1, lo .. pos
-    for (int64_t b = 32 * warp; b < n; b += 32 * kRowWarps) {
-        const int64_t i = b + lane;
-        const int64_t j = i < sinks ? i : lo + (i - sinks);
-        float s = -INFINITY;
-        int64_t off = -1;
-        if (i < n) {
-            const int page = page_of(p.kv, seq, j);
-            if (page >= 0) {
-                off = slot_offset(p.kv, page, hk, j);
-                const T* k = reinterpret_cast<const T*>(p.kv.k) + off;
-                s = 0.0f;
-                for (int d = 0; d < dim; d += 8) {
-                    float kk[8];
-                    load_f32<8>(k + d, kk);
+                    for (int e = 0; e < 8; ++e) x[e] = q[d + e];
+                },
+                r);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) s += q[d + e] * kk[e];
-                }
-                s *= p.scale_log2;
-            }
-        }
-        float mb = s;
-#pragma unroll
-        for (int w = 16; w >= 1; w >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
-        const float mn = fmaxf(m, mb);
-        const float a = exp2f(m - mn), pr = exp2f(s - mn);
-        l = l * a + pr;
-        m = mn;
-#pragma unroll
-        for (int e = 0; e < kMaxDim / 32; ++e) o[e] *= a;
-        for (int g = 0; g < 32; ++g) {
-            const float pg = __shfl_sync(0xffffffffu, pr, g);
-            const int64_t og = __shfl_sync(0xffffffffu, off, g);
-            if (og < 0) continue;
-            const T* v = reinterpret_cast<const T*>(p.kv.v) + og;
-#pragma unroll
-            for (int e = 0; e < kMaxDim / 32; ++e)
-                if (lane + 32 * e < dim) o[e] += pg * to_f32(v[lane + 32 * e]);
-        }
-    }
-#pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-    if (lane == 0) om[warp] = m, ol[warp] = l;
+    for (int w = 16; w >= 1; w >>= 1) r.l += __shfl_xor_sync(0xffffffffu, r.l, w);
+    if (lane == 0) om[warp] = r.m, ol[warp] = r.l;
 #pragma unroll
     for (int e = 0; e < kMaxDim / 32; ++e)
-        if (lane + 32 * e < dim) oo[warp][lane + 32 * e] = o[e];
+        if (lane + 32 * e < dim) oo[warp][lane + 32 * e] = r.o[e];
     __syncthreads();
     float M = -FLT_MAX, L = 0.0f, a[kRowWarps];
     for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, om[w]);
@@ -306,23 +265,65 @@ __device__ __forceinline__ bool consumers_agree(bool ok) {
     return all != 0;
 }
 
-// Four elements of row r of a tile (its sum o, not divided yet).
+// The consumers' barrier, and whether any thread came with `flag`.
+__device__ __forceinline__ bool consumers_any(bool flag) {
+    uint32_t any;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(any)
+        : "r"(flag ? 1u : 0u), "n"(32 * kSplitWarps)
+        : "memory");
+    return any != 0;
+}
+
+// Four elements of row r of a tile (its sum o, not divided yet).  True, where
+// `look`: one of them is infinite or no number though the sum of the row's
+// probabilities is neither.
 template <typename T, int DIM>
-__device__ __forceinline__ void write_four(const SplitParams& pp, const UnitInfo& tile, int r, int d, float M, float L, float4 v) {
+__device__ __forceinline__ bool write_four(const SplitParams& pp, const UnitInfo& tile, int r, int d, float M, float L, float4 v, bool look) {
     const AttnParams& p = pp.a;
     const int group = p.n_q_heads / p.kv.n_heads, rr = tile.r0 + r;
     const int64_t row = int64_t(tile.t0 + rr / group) * p.n_q_heads + tile.hk * group + rr % group;
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+    const bool odd = look && !(0.0f * (v.x + v.y + v.z + v.w) == 0.0f) && L == L;
     if (pp.part_o) {
         const int64_t at = row + (pp.prefix && !(tile.flags & kPrefix) ? int64_t(p.n_tokens) * p.n_q_heads : 0);
         *reinterpret_cast<float4*>(pp.part_o + at * DIM + d) = v;
         if (d == 0) pp.part_lse[at] = L == 0.0f ? -INFINITY : M + log2f(L);
-        return;
+        return odd;
     }
     if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * DIM + d) = v;
     else *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * DIM + d) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
     if (p.lse && d == 0) p.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    return odd;
+}
+// Such a row once more, by one warp.
+template <typename T, int DIM>
+__device__ __forceinline__ void four_again(const SplitParams& pp, const UnitInfo& tile, int r) {
+    const AttnParams& p = pp.a;
+    const int group = p.n_q_heads / p.kv.n_heads, rr = tile.r0 + r;
+    const int t = tile.t0 + rr / group, h = tile.hk * group + rr % group, seq = seq_of_token(p.kv, t);
+    if (seq < 0) return;
+    const bool prefix = tile.flags & kPrefix;
+    // the keys that were fetched and it does not see: later ones, and those of the first token's window before its own
+    const int64_t pos = position_of(p.kv, seq, t), room = p.kv.table_stride << p.kv.page_shift;
+    const int64_t end = prefix ? p.shared_len : p.kv.kv_len[seq], later = pos + 1 > 0 ? pos + 1 : 0;
+    const int64_t first = p.window > 0 ? position_of(p.kv, seq, p.kv.q_start[seq]) + 1 - p.window : 0;
+    if (!odd_values<T, DIM>(p, prefix ? 0 : seq, tile.hk, later > p.shared_len || prefix ? later : p.shared_len, end < room ? end : room) &&
+        !(p.window > 0 && odd_values<T, DIM>(p, seq, tile.hk, first > p.sinks ? first : p.sinks, pos + 1 - p.window)))
+        return;
+    const T* q = static_cast<const T*>(p.q) + int64_t(t) * p.q_stride + int64_t(h) * DIM;
+    RowSums<DIM / 32> sums;
+    row_sums<T, 4>(p, prefix ? 0 : seq, pos, tile.hk, prefix ? 0 : p.shared_len, prefix ? p.shared_len : INT64_MAX, 0, 32,
+                [&](int d, float (&x)[8]) { load_f32<8>(q + d, x); }, sums);
+    const int64_t row = int64_t(t) * p.n_q_heads + h;
+    if (pp.part_o) {
+        const int64_t at = row + (pp.prefix && !prefix ? int64_t(p.n_tokens) * p.n_q_heads : 0);
+        write_row_again<T, DIM>(sums, pp.part_o, true, at * DIM);
+    } else {
+        write_row_again<T, DIM>(sums, p.out, p.out_f32, row * DIM);
+    }
 }
 
 // (M, L) and (m, l) become one maximum and one sum.  Sums over scores that are
@@ -334,9 +335,9 @@ __device__ __forceinline__ void join_sums(float& M, float& L, float m, float l) 
 }
 
 // The parts of a tile that several workers shared, joined by the consumers of
-// the last of them to arrive.
+// the last of them to arrive.  The rows of which write_four says so, as bits.
 template <typename T, int DIM>
-__device__ __forceinline__ void join_parts(const SplitParams& pp, const UnitInfo& tile, float* buf) {
+__device__ __forceinline__ uint32_t join_parts(const SplitParams& pp, const UnitInfo& tile, float* buf, bool look) {
     float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(pp.a.scratch) + kCounterBytes);
     float* buf_ml = buf + kSplitWarps * 8 * DIM;
     const int live = tile.rows < kRows ? tile.rows : kRows, parts = tile.parts + 1;
@@ -372,6 +373,7 @@ __device__ __forceinline__ void join_parts(const SplitParams& pp, const UnitInfo
         if (i8 == 0) *reinterpret_cast<float2*>(buf_ml + 2 * r8) = make_float2(M, L);
     }
     consumers_sync();
+    uint32_t odd = 0;
     for (int x = threadIdx.x; x < live * (DIM / 4); x += 32 * kSplitWarps) {
         const int r = x / (DIM / 4), d = x % (DIM / 4) * 4;
         const float2 ml = *reinterpret_cast<const float2*>(buf_ml + 2 * r);
@@ -395,8 +397,9 @@ __device__ __forceinline__ void join_parts(const SplitParams& pp, const UnitInfo
                 acc.x += c * v[y].x, acc.y += c * v[y].y, acc.z += c * v[y].z, acc.w += c * v[y].w;
             }
         }
-        write_four<T, DIM>(pp, tile, r, d, ml.x, ml.y, acc);
+        if (write_four<T, DIM>(pp, tile, r, d, ml.x, ml.y, acc, look)) odd |= 1u << r;
     }
+    return odd;
 }
 
 template <typename T, int DIM>
@@ -757,7 +760,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
         if (left > 1 && ok) open_tile(info[slot]);
         const int rows = done.rows;  // (16 at most count)
         const auto part_at = [&](int i) -> float* { return partials + int64_t(i) * partial_floats<DIM>(); };
-        const auto finish = [&](int r, int d, float M, float L, float4 v) { write_four<T, DIM>(pp, done, r, d, M, L, v); };
+        const bool look = done.r0 + rows != group;  // (a sequence's only token sees all that was fetched)
+        uint32_t odd = 0;                           // rows that write_four found odd
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (8 * i >= rows) break;
@@ -793,7 +797,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                     acc.x += a * v.x, acc.y += a * v.y, acc.z += a * v.z, acc.w += a * v.w;
                 }
                 if (done.parts == 0) {
-                    finish(8 * i + r, d, M, L, acc);
+                    if (write_four<T, DIM>(pp, done, 8 * i + r, d, M, L, acc, look)) odd |= 1u << (8 * i + r);
                 } else {
                     float* to = part_at(int(blockIdx.x) == done.wf ? done.part : 2 * int(blockIdx.x));
                     *reinterpret_cast<float4*>(to + (8 * i + r) * DIM + d) = acc;
@@ -815,9 +819,20 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_kernel(const __gr
                 }
             }
             consumers_sync();
-            if (*last_flag) join_parts<T, DIM>(pp, done, buf);
+            if (*last_flag) odd = join_parts<T, DIM>(pp, done, buf, look);
         }
-        consumers_sync();  // the buffer is read
+        if (!look) {
+            consumers_sync();  // the buffer is read
+        } else if (consumers_any(odd != 0)) {
+            unsigned* const mask = reinterpret_cast<unsigned*>(buf);
+            if (threadIdx.x == 0) *mask = 0;
+            consumers_sync();
+            if (odd) atomicOr(mask, odd);
+            consumers_sync();
+            for (int r = warp; r < kRows; r += kSplitWarps)
+                if (*mask & (1u << r)) four_again<T, DIM>(pp, done, r);
+            consumers_sync();
+        }
     }
     if (!ok && together) consumers_agree(false);
     if (pp.beside) pdl_wait_prior_grid();  // complete only after that kernel, too

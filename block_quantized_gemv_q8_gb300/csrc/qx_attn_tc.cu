@@ -70,7 +70,8 @@ constexpr int kRescale = IsBf16<T>::value ? 8 : 2;
 constexpr int kFixed = 3;              // blocks that a pair's fixed cost (some 5 us) is worth
 constexpr int kMinPart = 8;            // blocks of a range at least: a part costs some 5 us beside them
 constexpr float kWritten = INFINITY;   // as a row's first base-2 log: the row is in the output already
-constexpr unsigned long long kWaitNs = 2000000000ull;
+// (long enough for rows_again() of 32 rows over a million keys, which the other warps wait for)
+constexpr unsigned long long kWaitNs = 10000000000ull;
 
 template <int DIM>
 struct TcGeom {
@@ -188,11 +189,13 @@ __device__ __forceinline__ uint32_t bits_from(int n) {
 // of shared memory: 128 bytes of every row at a time, so that eight lanes
 // write a row's 128 bytes together.  (Each lane writing its own row made 32
 // lines of every store: the epilogue took 8000 cycles, and the MMA issuer's
-// barrier accesses stood behind it.)  `left`: told when O has been read.
+// barrier accesses stood behind it.)  `left`: told when O has been read.  True:
+// an element of the warp's first rows is infinite or no number.
 template <int DIM, typename T>
-__device__ __forceinline__ void write_rows(T* dst, int64_t at, bool live, uint32_t o, bool some, float inv, uint8_t* stage, int lane,
+__device__ __forceinline__ bool write_rows(T* dst, int64_t at, bool live, uint32_t o, bool some, float inv, uint8_t* stage, int lane,
                                            uint64_t* left) {
     constexpr int E = 128 / int(sizeof(T));  // elements a pass
+    bool odd = false;
     if (!live) at = -1;
     T* to[8];  // of rows 4 k + lane / 8, this lane's 16 bytes
 #pragma unroll
@@ -236,7 +239,9 @@ __device__ __forceinline__ void write_rows(T* dst, int64_t at, bool live, uint32
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (to[k]) *reinterpret_cast<uint4*>(to[k] + x0) = w[k];
+        if (to[0]) odd |= any_odd<T>(w[0]);
     }
+    return __any_sync(0xffffffffu, odd);
 }
 
 // What a CTA works on: `tokens` tokens from t0 on (at most two tiles) of
@@ -468,6 +473,46 @@ __device__ __forceinline__ bool block_has_unseen(const TcWork& w, int i) {
     key_range<JOINT>(w, i, lo, hi);
     const int j0 = key_block<JOINT>(w, i);
     return j0 < lo || j0 + kKeys > hi;
+}
+// A row of the pair over its blocks in w once more, by one warp and over the keys
+// that the row sees alone.
+template <typename T, int DIM, bool JOINT>
+__device__ __forceinline__ void blocks_again(const TcAttnParams& p, const TcWork& w, int t, int h, int pos, RowSums<DIM / 32>& sums) {
+    const T* q = static_cast<const T*>(p.a.q) + int64_t(t) * p.a.q_stride + int64_t(h) * DIM;
+    for (int i = w.i0; i < w.i0 + w.nb; ++i) {
+        int lo, hi;
+        key_range<JOINT>(w, i, lo, hi);
+        for (int k = threadIdx.x & 31; k < kKeys; k += 32) {
+            int j = key_block<JOINT>(w, i) + k;
+            bool sees = j >= lo && j < hi;
+            if (JOINT && i == 0 && k < w.sinks) j = k, sees = true;
+            sees = sees && j <= pos && (p.a.window == 0 || j > pos - p.a.window || j < p.a.sinks);
+            if (__any_sync(0xffffffffu, sees))
+                row_keys<T, 8>(p.a, w.b, w.hk, sees ? j : -1, [&](int d, float (&x)[8]) { load_f32<8>(q + d, x); }, sums);
+        }
+    }
+}
+// The warp's rows `sound` (a lane each: token tok of the pair, at position pos,
+// head h, o / l from row `at` on) once more, where some of them do not see a
+// value that is infinite or no number: a later key's, or one of the first row's
+// window before their own.  (A call, not in line: the code of the rows' way out
+// stays as short as it was.  Causal 4096 tokens 104.5 us, in line 106.3 to 107,
+// without it 103.7.  Where it has work it takes its time: 7 us for 32 keys of a
+// row, 57 ms for 2000 tokens over 8192 keys whose last value is no number.)
+template <typename T, int DIM, bool JOINT>
+__device__ __noinline__ void rows_again(const TcAttnParams& p, const TcWork& w, unsigned sound, int low, int pos, int tok, int h, int64_t at,
+                                        bool to_part) {
+    __syncwarp();  // (the rows were written by other lanes)
+    low = __reduce_min_sync(0xffffffffu, low);
+    const int high = __reduce_max_sync(0xffffffffu, pos);
+    const int64_t from = p.a.sinks > w.lo ? p.a.sinks : w.lo, to = p.a.window > 0 ? high + 1 - p.a.window : 0;
+    if (!odd_values<T, DIM>(p.a, w.b, w.hk, low + 1 > w.lo ? low + 1 : w.lo, w.end) && !odd_values<T, DIM>(p.a, w.b, w.hk, from, to)) return;
+    for (unsigned again = sound; again != 0; again &= again - 1) {
+        const int src = __ffs(again) - 1;
+        RowSums<DIM / 32> sums;
+        blocks_again<T, DIM, JOINT>(p, w, w.t0 + __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), __shfl_sync(0xffffffffu, pos, src), sums);
+        write_row_again<T, DIM>(sums, to_part ? p.part_o : p.a.out, to_part || p.a.out_f32, __shfl_sync(0xffffffffu, at, src) * DIM);
+    }
 }
 __device__ __forceinline__ int count_pairs(const TcAttnParams& p, int lane) {
     const int pair = 2 * p.tile_tokens, seqs = tc_seqs(p);
@@ -935,9 +980,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             {
                 if (live && !to_part && p.a.lse) p.a.lse[row] = lse2 * 0.6931471805599453f;
                 uint8_t* stage = outs + warp * 4096;
-                if (to_part) write_rows<DIM>(p.part_o, part * DIM, live, oa, nb > 0, inv, stage, lane, &o_empty[t]);
-                else if (p.a.out_f32) write_rows<DIM>(static_cast<float*>(p.a.out), row * DIM, live, oa, nb > 0, inv, stage, lane, &o_empty[t]);
-                else write_rows<DIM>(static_cast<T*>(p.a.out), row * DIM, live, oa, nb > 0, inv, stage, lane, &o_empty[t]);
+                // A value that is infinite or no number shows in all rows, so the first ones tell.
+                bool odd;
+                if (to_part) odd = write_rows<DIM>(p.part_o, part * DIM, live, oa, nb > 0, inv, stage, lane, &o_empty[t]);
+                else if (p.a.out_f32) odd = write_rows<DIM>(static_cast<float*>(p.a.out), row * DIM, live, oa, nb > 0, inv, stage, lane, &o_empty[t]);
+                else odd = write_rows<DIM>(static_cast<T*>(p.a.out), row * DIM, live, oa, nb > 0, inv, stage, lane, &o_empty[t]);
+                // (where the sum of a row's probabilities is no number, no element of it is one)
+                const unsigned sound = __ballot_sync(0xffffffffu, live && l == l);
+                if (odd)
+                    rows_again<T, DIM, JOINT>(p, w, sound, live ? pos : INT32_MAX, pos, tok, head + w.hk * group, to_part ? part : row, to_part);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&w_empty[n & 1]);

@@ -441,8 +441,8 @@ qx_status qx_rope_append(const qx_kv* kv, const qx_qkv* in, const float* cos, co
  * f32 out carries that much too: relative 2^-8 for bf16 and 2^-11 for f16, at
  * most; f16 holds those below 2^-27 of the row's largest to 2^-38 of it.  At
  * other head sizes they stay in f32.
- * Slots of the cache that no token of its sequence sees have no effect,
- * whatever they hold (pages outside the window may be given back).
+ * A key that a row does not see has no effect on it, whatever its slot holds
+ * (NaN and infinities, too; pages outside the window may be given back).
  * scratch: device, qx_attn_scratch_bytes() of the same sizes, 256-byte
  * aligned, its first QX_ATTN_COUNTER_BYTES bytes zero-filled before its first
  * use; a completed call leaves it fit for the next.  After a bounded wait that

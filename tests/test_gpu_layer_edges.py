@@ -138,3 +138,59 @@ def test_block_norm_refuses_output_rows_that_overlap():
     assert torch.equal(r2, r[:1] + y)
     r2, _ = qx.qx_block_norm(y[:1], r[:1], r_out=torch.empty(64, device="cuda").as_strided((1, 64), (0, 1)))
     assert torch.equal(r2, r[:1] + y[:1]) and qx.qx_device_check() == qx.QX_OK
+
+
+@pytest.mark.parametrize("dim", [64, 128, 80])
+@pytest.mark.parametrize("out_dtype", [BF16, F32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q_lens,kv_lens,at,window,sinks", [
+    ([4], [40], 38, 0, 0), ([3, 2], [700, 30], 698, 0, 0), ([3], [6000], 5998, 0, 0), ([6], [300], 257, 40, 0), ([6], [300], 2, 40, 5),
+    ([140], [140], 100, 0, 0), ([140, 1], [400, 9], 300, 0, 0), ([150], [600], 430, 60, 3), ([130], [7000], 6990, 0, 0),
+    ([150], [600], 430, 60, 20), ([140, 3], [400, 9], 5, 0, 0), ([64, 64], [64, 192], 63, 0, 0), ([400], [400], 399, 0, 0), ([300], [300], 17, 30, 2)])
+def test_a_value_that_some_rows_do_not_see(dim, out_dtype, value, q_lens, kv_lens, at, window, sinks):
+    """Rows whose mask hides the key of an infinite or undefined value are as if it were not there."""
+    b = Batch(q_lens, kv_lens, 4, 2, dim, 16, BF16, seed=3)
+    b.v[int(b.table_host[0, at // 16]), 0, at % 16, 5:9] = value
+    lse = torch.empty((b.T, 4), device="cuda")
+    out = torch.empty((b.T, 4, dim), dtype=out_dtype, device="cuda")
+    qx.qx_attn_paged(b.kv, b.q, window=window, sinks=sinks, out=out, lse=lse)
+    assert qx.qx_device_check() == qx.QX_OK
+    o, l, mass, top = b.expect(dim ** -0.5, window, sinks)
+    pos = np.arange(kv_lens[0] - q_lens[0], kv_lens[0])
+    sees = (at <= pos) & ((window == 0) | (at > pos - window) | (at < sinks))
+    hit = np.zeros(o.shape, dtype=bool)
+    hit[:q_lens[0], :2, 5:9] = sees[:, None, None]
+    got = ref.f64(out)
+    assert np.array_equal(np.isfinite(got), ~hit)
+    # (the reference's rows that see it hold a finite value there: they are not compared in those elements)
+    err = np.where(hit, 0.0, np.abs(np.where(hit, 0.0, got) - o))
+    assert (err <= ref.attention_bound(o, mass, top, dim, BF16, out_dtype)).all()
+    assert (np.abs(ref.f64(lse) - l) <= ref.lse_bound(l, top, dim)).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("shared,tails,q_lens,at", [(300, [3, 9], [3, 9], 302), (300, [4, 100], [8, 100], 298), (5000, [6, 6], [3, 3], 5004),
+                                                    (5000, [200, 1], [200, 1], 5100)])
+def test_a_value_that_some_rows_do_not_see_behind_a_prefix(dim, shared, tails, q_lens, at):
+    kv_lens = [shared + t for t in tails]
+    b = Batch(q_lens, kv_lens, 4, 2, dim, 16, BF16, seed=4)
+    for n in range(1, len(kv_lens)):
+        b.keys[n][:shared], b.values[n][:shared] = b.keys[0][:shared], b.values[0][:shared]
+        for i in range(-(-shared // 16)):
+            m, src, dst = min(16, shared - 16 * i), int(b.table_host[0, i]), int(b.table_host[n, i])
+            b.k[dst, :, :m], b.v[dst, :, :m] = b.k[src, :, :m], b.v[src, :, :m]
+    owners = range(len(kv_lens)) if at < shared else [0]
+    for n in owners:
+        b.v[int(b.table_host[n, at // 16]), 1, at % 16, 11] = float("nan")
+    lse = torch.empty((b.T, 4), device="cuda")
+    out = qx.qx_attn_shared(b.kv, b.q, shared, lse=lse)
+    assert qx.qx_device_check() == qx.QX_OK
+    o, l, mass, top = b.expect(dim ** -0.5)
+    hit = np.zeros(o.shape, dtype=bool)
+    for t, n, pos in ref.tokens(kv_lens, b.q_start_host):
+        hit[t, 2:, 11] = n in owners and pos >= at
+    got = ref.f64(out)
+    assert np.array_equal(np.isfinite(got), ~hit)
+    err = np.where(hit, 0.0, np.abs(np.where(hit, 0.0, got) - o))
+    assert (err <= ref.attention_bound(o, mass, top, dim, BF16, BF16)).all()
+    assert (np.abs(ref.f64(lse) - l) <= ref.lse_bound(l, top, dim)).all()
