@@ -416,6 +416,22 @@ def _raw_stream(stream, index: int) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output for a call on `stream` (None: the current one).
+
+    It is the call's stream's memory: another stream's could still be in use
+    there, or be given to others there while the call writes it.  The current
+    stream, whose program holds it, is noted as a user."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _heads(t: torch.Tensor, shape: tuple, dtype, index: int, what: str) -> int:
     """Token stride of a [tokens, heads, dim] tensor on GPU `index` whose heads of a token lie one after another."""
     if t.get_device() != index:
@@ -571,7 +587,7 @@ def qx_rope_append(kv: PagedKV, q: torch.Tensor | None, k: torch.Tensor, v: torc
         if not (q.shape == (n, hq, dim) and q.dtype is dt and qb == dim and qc == 1 and q.get_device() == index):
             q_stride = _heads(q, (n, hq, dim), dt, index, "q")
         if q_out is None:
-            q_out = torch.empty((n, hq, dim), dtype=kv.dtype, device=kv.device)
+            q_out = _empty((n, hq, dim), kv.dtype, kv.device, stream)
         elif q_out.dtype != kv.dtype or q_out.shape != q.shape or not q_out.is_contiguous() or q_out.get_device() != index:
             raise ValueError("q_out: need a contiguous tensor on the cache's GPU, of q's shape and the cache's type")
         out = q_out.data_ptr()
@@ -602,7 +618,7 @@ def _attn(kv: PagedKV, q: torch.Tensor, scale, out, lse, stream):
     index = kv._index
     q_stride = _heads(q, (n, hq, kv.head_dim), kv.dtype, index, "q")
     if out is None:
-        out = torch.empty(shape, dtype=kv.dtype, device=kv.device)
+        out = _empty(shape, kv.dtype, kv.device, stream)
     elif out.shape != shape or not out.is_contiguous() or out.get_device() != index:
         raise ValueError("out: need a contiguous tensor on the cache's GPU, of q's shape")
     code = _DTYPE.get(out.dtype)
@@ -709,7 +725,7 @@ def qx_block_norm(y: torch.Tensor | None, r: torch.Tensor, w_post: torch.Tensor 
         r_out = r  # unchanged
     else:
         if r_out is None:
-            r_out = torch.empty(shape, dtype=res, device=r.device)
+            r_out = _empty(shape, res, r.device, stream)
         strides, ro_ptr = r_out.stride(), r_out.data_ptr()
         ro_stride = strides[0] if r_out.dtype is res and r_out.shape == shape and strides[1] == 1 and r_out.get_device() == index else \
             _rows(r_out, shape, res, index, "r_out")
@@ -718,7 +734,7 @@ def qx_block_norm(y: torch.Tensor | None, r: torch.Tensor, w_post: torch.Tensor 
         if not (w_pre.dtype is _F32 and w_pre.get_device() == index and w_pre.shape == (cols,) and w_pre.is_contiguous()):
             _vector(w_pre, cols, _F32, index, "w_pre")
         if x_out is None:
-            x_out = torch.empty(shape, dtype=act, device=r.device)
+            x_out = _empty(shape, act, r.device, stream)
         strides, x_ptr = x_out.stride(), x_out.data_ptr()
         x_stride = strides[0] if x_out.dtype is act and x_out.shape == shape and strides[1] == 1 and x_out.get_device() == index else \
             _rows(x_out, shape, act, index, "x_out")

@@ -194,3 +194,28 @@ def test_a_value_that_some_rows_do_not_see_behind_a_prefix(dim, shared, tails, q
     err = np.where(hit, 0.0, np.abs(np.where(hit, 0.0, got) - o))
     assert (err <= ref.attention_bound(o, mass, top, dim, BF16, BF16)).all()
     assert (np.abs(ref.f64(lse) - l) <= ref.lse_bound(l, top, dim)).all()
+
+
+def stream_of(t):
+    """The stream whose memory a tensor is, by the allocator's own account."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not the allocator's")
+
+
+@pytest.mark.parametrize("number", [False, True])
+def test_outputs_are_memory_of_the_calls_stream(number):
+    b = Batch([1, 2], [20, 33], 4, 2, 64, 16, BF16)
+    x, w = torch.randn(3, 8, 64, device="cuda"), torch.ones(512, device="cuda")
+    y = x.view(3, 512)
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if number else s
+    s.wait_stream(torch.cuda.current_stream())
+    outs = [qx.qx_rope_append(b.kv, x[:, :4], x[:, 4:6], x[:, 6:], stream=stream), qx.qx_attn_paged(b.kv, b.q, stream=stream),
+            qx.qx_attn_shared(b.kv, b.q, 0, stream=stream), *qx.qx_block_norm(y, y, w_pre=w, stream=stream)]
+    assert [stream_of(t) for t in outs] == [s.cuda_stream] * 5
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(outs[0], x[:, :4].to(BF16)) and torch.equal(outs[3], y + y)
+    assert stream_of(qx.qx_attn_paged(b.kv, b.q)) == torch.cuda.current_stream().cuda_stream
+    assert qx.qx_device_check() == qx.QX_OK
