@@ -879,7 +879,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 }
             }
             const int wlo = pos >= window ? pos - window + 1 : 0;  // first key of this row's window
-            float m = -INFINITY, l = 0.0f;
+            // (A thread without a row has whatever shared memory held as its scores:
+            // with this maximum it never asks for a rescale, which would move its
+            // warp's rows to other bases, and their outputs to other roundings.)
+            float m = live ? -INFINITY : INFINITY, l = 0.0f;
             float s[kKeys];
             const int nb = w.nb;
             for (int i = 0; i < nb; ++i) {

@@ -219,3 +219,22 @@ def test_outputs_are_memory_of_the_calls_stream(number):
     assert torch.equal(outs[0], x[:, :4].to(BF16)) and torch.equal(outs[3], y + y)
     assert stream_of(qx.qx_attn_paged(b.kv, b.q)) == torch.cuda.current_stream().cuda_stream
     assert qx.qx_device_check() == qx.QX_OK
+
+
+@pytest.mark.parametrize("heads", [(14, 2, 64), (12, 2, 128), (5, 1, 128), (10, 1, 64), (3, 3, 64)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_the_same_inputs_give_the_same_bits(heads, dtype):
+    """Whatever other kernels left in shared memory, where a tile's rows are not all tokens' rows."""
+    hq, hkv, dim = heads
+    for q_lens, kv_lens in (([150, 40], [2000, 300]), ([700], [900]), ([70] * 9, list(range(70, 700, 70)))):
+        b = Batch(q_lens, kv_lens, hq, hkv, dim, 16, dtype, seed=6)
+        first = None
+        for n in range(8):
+            y = torch.randn((2000, 4096), device="cuda") * 10.0 ** (n - 4)  # (a ring of rows in shared memory)
+            qx.qx_block_norm(y, y, w_pre=torch.ones(4096, device="cuda"))
+            lse = torch.empty((b.T, hq), device="cuda")
+            out = qx.qx_attn_paged(b.kv, b.q, lse=lse)
+            if first is None:
+                first = out, lse
+                b.check(out, lse, b.expect(dim ** -0.5))
+            assert torch.equal(out.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1])
