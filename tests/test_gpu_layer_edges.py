@@ -6,7 +6,7 @@ import torch
 
 import block_quantized_gemv_q8_gb300 as qx
 from . import layer_reference as ref
-from .test_gpu_layer import BF16, F16, F32, Batch, table_of
+from .test_gpu_layer import BF16, F16, F32, Batch, check_norm, table_of
 
 pytestmark = pytest.mark.gpu
 
@@ -238,3 +238,15 @@ def test_the_same_inputs_give_the_same_bits(heads, dtype):
                 first = out, lse
                 b.check(out, lse, b.expect(dim ** -0.5))
             assert torch.equal(out.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("act,res", [(BF16, F16), (F32, F16), (F16, BF16), (F32, BF16)])
+@pytest.mark.parametrize("rows,cols", [(3, 1000), (1300, 2048), (2, 14336)])
+def test_block_norm_of_other_pairs_of_types(act, res, rows, cols):
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    make = lambda *shape, dt=F32: torch.empty(shape, device="cuda").normal_(generator=g).to(dt)  # noqa: E731
+    y, r, gate, w1, w2 = make(rows, cols, dt=act), make(rows, cols, dt=res), make(rows, cols, dt=act), make(cols), make(cols)
+    r2, x = qx.qx_block_norm(y, r, w_post=w1, gate=gate, alpha=0.7, w_pre=w2)
+    assert r2.dtype == res and x.dtype == act
+    some = slice(0, 40)
+    check_norm(y[some], r[some], w1, gate[some], 0.7, w2, 1e-5, r2[some], x[some])
