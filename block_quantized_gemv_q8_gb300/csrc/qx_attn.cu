@@ -19,9 +19,10 @@ constexpr int kMaxDim = QX_MAX_HEAD_DIM;
 // Any head size: one CTA per row, its warps taking blocks of 32 keys in turn
 // (a lane scores a key, then owns every 32nd output element), joined at the
 // end.  It serves the head sizes that the kernels below do not (all but 64 and
-// 128) and reads a key once for every row: 64 tokens over windows of 4096 keys
-// take it 1.91 ms, where the split kernel takes 0.15.  (8 tokens over 2000 keys,
-// head size 80: 301 us; with the values' loads past a branch 400.)
+// 128), keeps the probabilities in f32, and reads a key once for every row: 8
+// tokens over 2000 keys, 32 query heads of 80 over 8, take it 299 us (with the
+// values' loads past a branch 400), where the split kernel takes 20.5 at head size
+// 128.
 template <typename T>
 __global__ void __launch_bounds__(32 * kRowWarps, 8) attn_row_kernel(const __grid_constant__ AttnParams p) {
     __shared__ float q[kMaxDim];
@@ -90,9 +91,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, 8) attn_row_kernel(const __gri
 // group fills at most partly; the tensor pipe is not what bounds this kernel.
 //
 // Measured: 64 tokens over windows of 4096 keys (8 key heads of 128, bf16, 0.94
-// GB) 150 us, 6.3 TB/s, 92 % of the measured copy rate; 256 over up to 1000 keys
-// 98 us (80 %: a tile has eight units, and its join and its queries' way cost
-// about two); one over 131072 keys 92 us (86 %); one over 1023 keys 8 us, of
+// GB) 149 us, 6.3 TB/s, 93 % of the measured copy rate; 256 over up to 1000 keys
+// 97 us (81 %: a tile has eight units, and its join and its queries' way cost
+// about two); one over 131072 keys 91 us (87 %); one over 1023 keys 7.7 us, of
 // which 2 us are spent finding the worker's place and 3 us joining.
 
 constexpr int kUnit = 64;                // keys of a unit

@@ -24,21 +24,21 @@
 // what bounds a block, at about 2900 cycles.  Measured: 4096 causal tokens, 32
 // query heads of 128 over 8, 104 us, 1.32 PFLOP/s of the visible pairs, 68 % of
 // the measured bf16 rate; 8191 tokens over a window of 1024 keys and 4 first ones
-// 125 us (whole blocks at both ends of the window and for the first keys: 10.5
-// blocks where 8 hold visible keys); head size 64, 14 query heads over 2, 50 us
-// (the same chain for half the products).
+// 119 us (whole blocks at both ends of the window: 9 blocks where 8 hold visible
+// keys); head size 64, 14 query heads over 2, 49.5 us (the same chain for half the
+// products).
 //
 // The CTAs are persistent, one an SM.  Where there are many pairs they take them
 // from a counter, those with the most keys first; where there are few (a short
 // chunk, a shared prefix, contexts of very different lengths) each takes an
 // equal share of the line of all pairs' blocks.  A pair whose keys several CTAs
 // share leaves parts (o / l and the base-2 log of its sum) that
-// attn_join_kernel joins.  (256 tokens behind 32768 shared keys, 8 key heads: 32
-// pairs, each in four parts on 128 SMs 199 us with the tails, in even shares on
-// all 183.)  A third warpgroup serves the two: a scheduler, a
-// producer that runs ahead with the copies, a warp that issues the MMAs, and one
-// that zeroes values that no row sees.  The next pair's first scores are
-// computed during this pair's epilogue.
+// attn_join_kernel joins.  (256 tokens behind 32768 shared keys, 8 key heads, are
+// 32 pairs.  With the tails, each pair in four parts, on 128 of the SMs: 199 us; in
+// even shares on all of them: 182 us.)  A third warpgroup serves the two: a
+// scheduler, a producer that runs ahead with the copies, a warp that issues the
+// MMAs, and one that zeroes values that no row sees.  The next pair's first
+// scores are computed during this pair's epilogue.
 //
 // Every wait is bounded and reports through the device error word.
 #include <cuda.h>
