@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 8) attn_row_kernel(const __gri
 // which 2 us are spent finding the worker's place and 3 us joining.
 
 constexpr int kUnit = 64;                // keys of a unit
-constexpr uint64_t kSplitWaitNs = 2000000000ull;
+constexpr uint64_t kSplitWaitNs = 10000000000ull;  // (four_again() over millions of keys may be waited for)
 constexpr int kSplitWarps = 4;
 // A second warpgroup for the producer (its other three warps only give up
 // registers): 128 registers a thread at launch, of which the consumers, who hold
