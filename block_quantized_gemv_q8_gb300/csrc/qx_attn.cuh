@@ -22,7 +22,7 @@ struct IsBf16<__nv_bfloat16> {
 // to T, where the running maximum may be BEHIND the row's by so many (their sums
 // are raised with them, and o / l stays as it is).  f16 holds up to 2^15 and
 // loses bits below 2^-14: so raised, a probability keeps them down to 2^-29 of
-// the row's largest (2^-27 with 2 behind).
+// the row's largest (2^-26 with 3 behind).
 template <typename T, int BEHIND>
 constexpr float kLift = IsBf16<T>::value ? 0.0f : float(15 - BEHIND);
 

@@ -63,10 +63,11 @@ constexpr int kSoftmaxWarps = 8;       // two warpgroups
 constexpr int kTcThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "registers the CTA was launched with");
-// (f16: 2 leaves room to raise P by 2^13.  Five chunks of prompts in f16: 63.8 us,
-// 62.4 with 8 and no room.)
+// (f16: 3 leaves room to raise P by 2^12.  Causal 4096 tokens, and five chunks of
+// prompts at head size 64, in f16: 105.1 and 63.0 us; with 2 107.3 and 64.2, with 4
+// 104.4 and 62.6.)
 template <typename T>
-constexpr int kRescale = IsBf16<T>::value ? 8 : 2;
+constexpr int kRescale = IsBf16<T>::value ? 8 : 3;
 constexpr int kFixed = 3;              // blocks that a pair's fixed cost (some 5 us) is worth
 constexpr int kMinPart = 8;            // blocks of a range at least: a part costs some 5 us beside them
 constexpr float kWritten = INFINITY;   // as a row's first base-2 log: the row is in the output already

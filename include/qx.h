@@ -439,7 +439,7 @@ qx_status qx_rope_append(const qx_kv* kv, const qx_qkv* in, const float* cos, co
  * Scores, maxima, sums and outputs are held in f32.  At head sizes 64 and 128
  * the probabilities are rounded to the cache's type before they meet v, so an
  * f32 out carries that much too: relative 2^-8 for bf16 and 2^-11 for f16, at
- * most; f16 holds those below 2^-27 of the row's largest to 2^-38 of it.  At
+ * most; f16 holds those below 2^-26 of the row's largest to 2^-37 of it.  At
  * other head sizes they stay in f32.
  * A key that a row does not see has no effect on it, whatever its slot holds
  * (NaN and infinities, too; pages outside the window may be given back).
