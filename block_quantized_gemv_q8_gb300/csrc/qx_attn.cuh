@@ -31,6 +31,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// l r^2, for r = exp2_approx(x / 2): l 2^x where 2^x, which is r^2, may be below
+// f32's numbers though l 2^x is not.
+__device__ __forceinline__ float twice(float l, float r) { return l * r * r; }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

@@ -30,7 +30,10 @@ __device__ __forceinline__ float power_of_two(int exponent_field) { return __uin
 // A row's probabilities are multiplied by its values' scales before they are
 // rounded, so its running base is the largest score plus the least power of two
 // that no scale reaches (from 2^-80 on): so much are the probabilities and their
-// sum raised, and the products stay below the base's 1.
+// sum raised, and the products stay below the base's 1.  The base may be 80 powers
+// below the row's largest score, where its sum is up to 2^95 a key, or as much
+// above it as the scales are large; a sum goes from one base to the other whole
+// (twice(), qx_attn.cuh), while products that many powers down are nothing.
 constexpr float kLeastPower = -80.0f;
 __device__ __forceinline__ float scale_power(float d) {
     return fmaxf(float(int(__float_as_uint(d) >> 23 & 0xff) - 126), kLeastPower);

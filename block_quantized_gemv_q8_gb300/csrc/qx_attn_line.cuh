@@ -296,16 +296,19 @@ __device__ __forceinline__ bool write_four(const SplitParams& pp, const UnitInfo
     return odd;
 }
 // (M, L) and (m, l) become one maximum and one sum.  Sums over scores that are
-// no numbers have a maximum of -inf, and stay what they are.
+// no numbers have a maximum of -inf, and stay what they are.  FAR: the maxima
+// count more than the scores, so a lower one's sum may weigh as much.
+template <bool FAR>
 __device__ __forceinline__ void join_sums(float& M, float& L, float m, float l) {
     const float mn = fmaxf(M, m), base = mn == -INFINITY ? 0.0f : mn;
-    L = L * exp2_approx(M - base) + l * exp2_approx(m - base);
+    if constexpr (FAR) L = twice(L, exp2_approx(0.5f * (M - base))) + twice(l, exp2_approx(0.5f * (m - base)));
+    else L = L * exp2_approx(M - base) + l * exp2_approx(m - base);
     M = mn;
 }
 
 // The parts of a tile that several workers shared, joined by the consumers of
 // the last of them to arrive.  The rows of which write_four says so, as bits.
-template <typename T, int DIM, int ROWS = kRows>
+template <typename T, int DIM, int ROWS = kRows, bool FAR = false>
 __device__ __forceinline__ uint32_t join_parts(const SplitParams& pp, const UnitInfo& tile, float* buf, bool look) {
     float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(pp.a.scratch) + kCounterBytes);
     float* buf_ml = buf + kSplitWarps * 8 * DIM;
@@ -327,14 +330,14 @@ __device__ __forceinline__ uint32_t join_parts(const SplitParams& pp, const Unit
 #pragma unroll 4
             for (int i = i8; i < parts; i += 8) {
                 const float2 ml = __ldcg(reinterpret_cast<const float2*>(src(i) + ROWS * DIM + 2 * r8));
-                join_sums(M, L, ml.x, ml.y);
+                join_sums<FAR>(M, L, ml.x, ml.y);
                 if (fits) weight[r8 * parts + i] = ml.x;
             }
         }
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) {
             const float om = __shfl_xor_sync(0xffffffffu, M, o), ol = __shfl_xor_sync(0xffffffffu, L, o);
-            join_sums(M, L, om, ol);
+            join_sums<FAR>(M, L, om, ol);
         }
         if (r8 < live) {
             if (fits)

@@ -383,8 +383,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_q8_kernel(const _
                         float top = fmaxf(m[t][i], mx[t][i] + scale_power(d));
 #pragma unroll
                         for (int w = 4; w <= 16; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                        const float a = top == -INFINITY ? 1.0f : exp2_approx(m[t][i] - top);
-                        l[t][i] *= a;
+                        const float h = top == -INFINITY ? 1.0f : exp2_approx(0.5f * (m[t][i] - top)), a = h * h;
+                        l[t][i] = twice(l[t][i], h);
                         m[t][i] = top;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) o[k][t][i] *= a, o[k][t][2 + i] *= a;
@@ -478,9 +478,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_q8_kernel(const _
                 float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int w = 0; w < kSplitWarps; ++w) {
-                    const float a = ml[w].x == -INFINITY ? 0.0f : exp2_approx(ml[w].x - M);
+                    const float h = ml[w].x == -INFINITY ? 0.0f : exp2_approx(0.5f * (ml[w].x - M)), a = h * h;
                     const float4 v = *reinterpret_cast<const float4*>(buf + (8 * w + r) * DIM + (d ^ (8 * r)));
-                    L += a * ml[w].y;
+                    L += twice(ml[w].y, h);
                     acc.x += a * v.x, acc.y += a * v.y, acc.z += a * v.z, acc.w += a * v.w;
                 }
                 if (done.parts == 0) {
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_q8_kernel(const _
                 }
             }
             consumers_sync();
-            if (*last_flag) join_parts<T, DIM, ROWS>(pp, done, buf, false);
+            if (*last_flag) join_parts<T, DIM, ROWS, true>(pp, done, buf, false);
         }
         consumers_sync();  // the buffer is read, and the next tile's queries are there
     }

@@ -1142,8 +1142,15 @@ __global__ void __launch_bounds__(Q8 ? kTcThreadsQ8 : kTcThreads, 1) attn_tc_ker
                 if constexpr (Q8) top += power;
                 if (__any_sync(0xffffffffu, top > m + float(kRescale<P>))) {
                     const float mn = fmaxf(m, top);
-                    const float a = mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
-                    l *= a;
+                    float a;
+                    if constexpr (Q8) {
+                        const float h = mn == -INFINITY ? 1.0f : exp2_approx(0.5f * (m - mn));
+                        a = h * h;
+                        l = twice(l, h);
+                    } else {
+                        a = mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
+                        l *= a;
+                    }
                     m = mn;
                     if (i > 0) {
                         if (!(ok = warp_wait(&o_full[t], (blocks - 1) & 1, kv.err, kErrTimeoutMma))) break;
