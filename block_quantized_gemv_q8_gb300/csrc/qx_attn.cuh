@@ -35,6 +35,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // f32's numbers though l 2^x is not.
 __device__ __forceinline__ float twice(float l, float r) { return l * r * r; }
 
+// The scale of the scores over codes as two factors, their product: one of at most
+// 1, which goes to a key's scale, and one of at least 1, for the score that this
+// makes of q . c.  So neither leaves f32 where the score does not, and a product of
+// nothing is a score of nothing.
+__device__ __forceinline__ float inner_scale(float scale) { return fminf(fmaxf(scale, -1.0f), 1.0f); }
+__device__ __forceinline__ float outer_scale(float scale) { return fmaxf(fabsf(scale), 1.0f); }
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -91,9 +98,11 @@ __device__ __forceinline__ void row_keys(const AttnParams& p, int seq, int hk, i
                 const int64_t at = scale_offset(p.kv, page, hk, j);
                 const float dk = p.kv.k_scale[at];
                 dv = p.kv.v_scale[at];
-                s *= fabsf(dk) < INFINITY && fabsf(dv) < INFINITY ? dk : __uint_as_float(0x7fffffffu);
+                s *= fabsf(dk) < INFINITY && fabsf(dv) < INFINITY ? dk * inner_scale(p.scale_log2) : __uint_as_float(0x7fffffffu);
+                s *= outer_scale(p.scale_log2);
+            } else {
+                s *= p.scale_log2;
             }
-            s *= p.scale_log2;
         }
     }
     float mb = s;

@@ -329,13 +329,23 @@ __global__ void __launch_bounds__(kSplitThreads, 2) attn_split_q8_kernel(const _
                     float d = sc[16 * h + 8 * x], e = sc[kUnit + 16 * h + 8 * x];
                     const bool sound = fabsf(d) < INFINITY && fabsf(e) < INFINITY;
                     dv[h][x] = sound ? e : 0.0f;
-                    const float f = sound ? d * p.scale_log2 : __uint_as_float(0x7fffffffu);
+                    const float f = sound ? d * inner_scale(p.scale_log2) : __uint_as_float(0x7fffffffu);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        s[h][t][2 * x] *= kBf16 ? f * rows_f[t].x : f;
-                        s[h][t][2 * x + 1] *= kBf16 ? f * rows_f[t].y : f;
+                        if (kBf16) s[h][t][2 * x] *= rows_f[t].x, s[h][t][2 * x + 1] *= rows_f[t].y;
+                        s[h][t][2 * x] *= f;
+                        s[h][t][2 * x + 1] *= f;
                     }
                 }
+            if (fabsf(p.scale_log2) > 1.0f) {
+                const float f = outer_scale(p.scale_log2);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[h][t][x] *= f;
+            }
             const bool sink_unit = flags & kSink;
             if (j0 < lo || j0 + 32 > hi || j0 + 31 > pos_first || (!sink_unit && pos_last - window >= j0)) {
                 // some row does not see some of them

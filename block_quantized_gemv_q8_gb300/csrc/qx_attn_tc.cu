@@ -626,7 +626,7 @@ __device__ __forceinline__ void convert_blocks(const TcAttnParams& p, TcWork* wo
                     float* const sc = scales + set * G::kScaleFloats;
                     const float d = sound ? dv : 0.0f;
                     const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(d)));
-                    sc[key] = sound ? dk : __uint_as_float(0x7fffffffu);
+                    sc[key] = sound ? dk * inner_scale(p.a.scale_log2) : __uint_as_float(0x7fffffffu);
                     sc[kKeys + key] = d;
                     const int least = __reduce_min_sync(0xffffffffu, key_of(i) < 0 ? 128 : int(scale_power(fabsf(d))));
                     if (lane == 0) sc[2 * kKeys + part] = scale_power(__uint_as_float(most)), sc[2 * kKeys + 4 + part] = float(least);
@@ -1032,7 +1032,7 @@ __global__ void __launch_bounds__(Q8 ? kTcThreadsQ8 : kTcThreads, 1) attn_tc_ker
         const int in_tile = r / group, head = r - in_tile * group, tok = t * p.tile_tokens + in_tile;
         const int window = p.a.window > 0 && p.a.window < INT32_MAX ? int(p.a.window) : INT32_MAX;
         const int sinks = p.a.sinks < INT32_MAX ? int(p.a.sinks) : INT32_MAX;
-        const float f = p.a.scale_log2;  // positive: the split kernel takes the others
+        const float f = Q8 ? outer_scale(p.a.scale_log2) : p.a.scale_log2;  // positive: the split kernel takes the others
         uint32_t blocks = 0;             // of this tile so far
         uint32_t set = 0, set_phase = 0; // Q8: of the CTA's, whichever tiles they were for
         bool ok = true;

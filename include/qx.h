@@ -529,7 +529,9 @@ qx_status qx_kv_read_q8(const qx_kv_q8* kv, int64_t n_tokens, void* k_out, void*
  * the same scratch (qx_attn_scratch_bytes).  Row (t, h)
  *     out = sum_j p_j d^v_j c^v_j / sum_j p_j,   p_j = exp(scale d^k_j q . c^k_j).
  * over the keys that qx_attn_paged lets it see.  Queries and codes are taken as they
- * are; scores, maxima, sums and outputs are held in f32.  At head sizes 64 and 128
+ * are; scores, maxima, sums and outputs are held in f32.  q . c^k_j is summed up first;
+ * where that sum and the score are in f32's range, the factors between them are of any
+ * size (a sum of zero is a score of zero).  At head sizes 64 and 128
  * p_j d^v_j is rounded to f16 (relative 2^-11 at most) before it meets the codes;
  * products below 2^-21 of the row's largest p_j times its largest d^v_j are held to
  * 2^-32 of that, for value scales from 2^-100 to 2^100.  At other head sizes it
