@@ -34,6 +34,8 @@ __device__ __forceinline__ float power_of_two(int exponent_field) { return __uin
 // below the row's largest score, where its sum is up to 2^95 a key, or as much
 // above it as the scales are large; a sum goes from one base to the other whole
 // (twice(), qx_attn.cuh), while products that many powers down are nothing.
+// (2^-80: with a power of 2^-100 the sum, of 2^115 a key, would leave f32 at 8192
+// keys.  Values whose scales are all below 2^-80 keep what f16 leaves of them.)
 constexpr float kLeastPower = -80.0f;
 __device__ __forceinline__ float scale_power(float d) {
     return fmaxf(float(int(__float_as_uint(d) >> 23 & 0xff) - 126), kLeastPower);

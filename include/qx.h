@@ -533,10 +533,11 @@ qx_status qx_kv_read_q8(const qx_kv_q8* kv, int64_t n_tokens, void* k_out, void*
  * where that sum and the score are in f32's range, the factors between them are of any
  * size (a sum of zero is a score of zero).  At head sizes 64 and 128
  * p_j d^v_j is rounded to f16 (relative 2^-11 at most) before it meets the codes;
- * products below 2^-21 of the row's largest p_j times its largest d^v_j are held to
- * 2^-32 of that, for value scales from 2^-100 to 2^100.  At other head sizes it
- * stays in f32.  However far apart the value scales of a row's keys lie in that
- * range, the sum of its p_j holds all of them down to 2^-38 of the largest.
+ * products below 2^-21 of D, the row's largest p_j times its largest d^v_j (or 2^-80,
+ * where all of them are smaller), are held to 2^-32 of D, and the sum of the p_j holds
+ * all of them down to 2^-38 of the largest: for value scales up to 2^100, however far
+ * apart.  Smaller ones than 2^-80 alone so lose bits, below 2^-112 all of them.  At
+ * other head sizes it stays in f32.
  * A key that a row does not see has no effect on it, whatever its slot holds.  One
  * that it sees, and whose scale or whose value's scale is infinite or no number,
  * makes the row no numbers.

@@ -100,3 +100,33 @@ def test_sums_where_value_scales_lie_far_apart(heads, q_lens, kv_lens, low, high
         check(b, what=name)
         if name == "thirty-twos":
             check(b, window=70, sinks=3, what=name + ", window")
+
+
+@pytest.mark.parametrize("heads,q_lens,kv_lens", CASES, ids=lambda v: str(v))
+def test_value_scales_of_one_size(heads, q_lens, kv_lens):
+    """From 2^-80 to 2^100 relative to themselves; smaller ones as if they were 2^-80."""
+    for i, power in enumerate((-80, 100, -70, -100, -120)):
+        b = BatchQ8(q_lens, kv_lens, *heads, 16, (BF16, F16)[i % 2], seed=40 + i, k_std=3.0)
+        for s in range(len(kv_lens)):
+            d = scales_of(b, "v", s).astype(np.float64)
+            set_heads(b, "v", s, d / (d.max() if power > 0 else d.min()) * 2.0 ** power)
+        check(b, what=f"2^{power}")
+
+
+@pytest.mark.parametrize("heads,tokens", [((8, 2, 128), 1), ((14, 2, 64), 1), ((8, 1, 128), 64), ((4, 2, 80), 1)], ids=str)
+def test_many_small_probabilities_of_small_value_scales(heads, tokens):
+    """20000 keys of 2^-18 of the largest probability each, all value scales at 2^-80."""
+    kv = 20000
+    b = BatchQ8([tokens], [kv], *heads, 64, BF16, seed=50, spread=0.2)
+    b.q.fill_(1.0)
+    scales = np.zeros((kv, b.hkv))
+    codes = np.zeros((kv, b.hkv, b.dim))
+    codes[7] = 127
+    scales[7] = 18 * np.log(2) / (127 * b.dim * b.dim ** -0.5)
+    b.held["k"][0] = codes * scales_of(b, "k", 0)[..., None].astype(np.float64)
+    page, slot = slots(b, 0)
+    b.k[page, :, slot] = torch.from_numpy(codes).to(torch.int8).cuda()
+    set_heads(b, "k", 0, scales)
+    d = scales_of(b, "v", 0).astype(np.float64)
+    set_heads(b, "v", 0, d / d.min() * LEAST)
+    check(b)
