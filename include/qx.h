@@ -538,9 +538,11 @@ qx_status qx_kv_read_q8(const qx_kv_q8* kv, int64_t n_tokens, void* k_out, void*
  * all of them down to 2^-38 of the largest: for value scales up to 2^100, however far
  * apart.  Smaller ones than 2^-80 alone so lose bits, below 2^-112 all of them.  At
  * other head sizes it stays in f32.
- * A key that a row does not see has no effect on it, whatever its slot holds.  One
- * that it sees, and whose scale or whose value's scale is infinite or no number,
- * makes the row no numbers.
+ * A key that a row does not see does not enter it, whatever its slot holds (NaN and
+ * infinities, too), and the bounds above are of the keys that it sees; in which
+ * power of two its products are rounded may go by other rows and keys, so a row's
+ * last bits may.  One that it sees, and whose scale or whose value's scale is infinite
+ * or no number, makes the row no numbers.
  */
 qx_status qx_attn_paged_q8(const qx_kv_q8* kv, const void* q, int64_t n_tokens, int n_q_heads, int64_t q_stride,
                            float scale, int64_t window, int64_t sinks, void* out, qx_dtype out_dtype, float* lse,

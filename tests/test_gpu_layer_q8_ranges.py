@@ -130,3 +130,16 @@ def test_many_small_probabilities_of_small_value_scales(heads, tokens):
     d = scales_of(b, "v", 0).astype(np.float64)
     set_heads(b, "v", 0, d / d.min() * LEAST)
     check(b)
+
+
+@pytest.mark.parametrize("heads,q_lens,kv_lens", CASES, ids=lambda v: str(v))
+def test_value_scales_that_rise_from_key_to_key(heads, q_lens, kv_lens):
+    """Keys that a row does not see yet, or not any more, have larger values: the row is within the
+    bound of those that it sees."""
+    for i, rise in enumerate((lambda j: j // 16, lambda j: j % 128 // 32, lambda j: 60 - j // 16, lambda j: 4 * (j % 64 > 40))):
+        b = BatchQ8(q_lens, kv_lens, *heads, 16, (F16, BF16)[i % 2], seed=70 + i, k_std=2.0)
+        for s, kv in enumerate(kv_lens):
+            power = np.clip(rise(np.arange(kv)), -70, 90)
+            set_heads(b, "v", s, scales_of(b, "v", s).astype(np.float64) * 2.0 ** power[:, None])
+        check(b)
+        check(b, window=50, sinks=2, what="window")
