@@ -1075,11 +1075,17 @@ __global__ void __launch_bounds__(Q8 ? kTcThreadsQ8 : kTcThreads, 1) attn_tc_ker
             const int nb = w.nb;
             for (int i = 0; i < nb; ++i) {
                 const float* const sc = scales + set * G::kScaleFloats;
-                if constexpr (Q8) {  // (there before the scores)
+                if (!(ok = warp_wait(&s_full[t], blocks & 1, kv.err, kErrTimeoutMma))) break;
+                if constexpr (Q8) {
+                    // (Behind the scores, which the converters' keys were awaited for: the set
+                    // has been filled, and is not filled again before this block's values
+                    // have been multiplied, so its barrier is in the phase that is asked for.
+                    // Before them it may be two uses behind, where this warpgroup had no rows
+                    // for a while, and of the same parity.  Asked there, 512 tokens over 16384
+                    // keys took 189 us for 180, and 8191 tokens over the window 195 for 197.)
                     if (!(ok = warp_wait(&scale_full[set], set_phase, kv.err, kErrTimeoutMma))) break;
                     if (++set == G::kScaleSets) set = 0, set_phase ^= 1;
                 }
-                if (!(ok = warp_wait(&s_full[t], blocks & 1, kv.err, kErrTimeoutMma))) break;
                 tc_after();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) ld32(sa + 32 * c, s + 32 * c);
