@@ -640,10 +640,8 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
     }
     const int group = p.n_q_heads / p.kv.n_heads;
     const int64_t rows = int64_t(p.n_tokens) * p.n_q_heads;
-    float* part_lse = reinterpret_cast<float*>(static_cast<char*>(p.scratch) + kSplitScratch);
-    float* part_o = part_lse + part_rows(rows);
+    const Parts parts = parts_of(p, sm_count);
     // a scale that is not positive is an oddity that only the split kernel serves
-    unsigned* counter = static_cast<unsigned*>(p.scratch) + kMaxWorkers;
     if (rows > kMaxSharedRows || p.n_tokens < 2 || p.scale_log2 <= 0.0f) p.shared_len = 0;
     // Rows of a key head a sequence, on average: the split kernel reads a
     // sequence's keys once for every 16 of them, the tensor cores' once for
@@ -651,11 +649,10 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
     const bool many = int64_t(p.n_tokens) * group >= 64 * int64_t(p.kv.n_seqs) && p.scale_log2 > 0.0f;
     JoinParams j;
     j.a = p;
-    j.part_o = part_o;
-    j.part_lse = part_lse;
+    j.part_o = parts.o;
+    j.part_lse = parts.lse;
     j.parts = 0;
     cudaError_t e;
-    const int64_t spare = part_rows(rows);
     if (p.shared_len > 0) {
         // A short prefix for few rows: the split kernel takes it with the
         // tails, though it reads it once for every 16 rows.  (16 sequences
@@ -665,27 +662,23 @@ cudaError_t launch_attn(int dtype, const AttnParams& params, int sm_count, cudaS
         const int64_t units = (int64_t(p.n_tokens) * group + kRows - 1) / kRows * p.kv.n_heads * ((p.shared_len + kUnit - 1) / kUnit);
         if (!many && p.shared_len <= kShortPrefix && units <= int64_t(kPrefixUnits) * 2 * sm_count) {
             j.parts = 2;
-            e = launch_split_any(dtype, p, part_o, part_lse, false, true, sm_count, s);
+            e = launch_split_any(dtype, p, parts.o, parts.lse, false, true, sm_count, s);
             return e != cudaSuccess ? e : launch_attn_join(dtype, j, s);
         }
         // the prefix, the tails beside it, and both joined
-        const int slots = slots_for(0, (p.shared_len + 127) / 128, 1, rows, spare - rows, sm_count);
-        if ((e = launch_attn_tc(dtype, p, true, slots, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
+        const int slots = slots_for(0, (p.shared_len + 127) / 128, 1, rows, part_rows(rows) - rows, sm_count);
+        if ((e = launch_attn_tc(dtype, p, true, slots, parts.o, parts.lse, parts.counter, sm_count, s)) != cudaSuccess) return e;
         j.parts = slots > 0 ? slots : 1;
-        float* o = part_o + j.parts * rows * dim;
-        float* l = part_lse + j.parts * rows;
+        float* o = parts.o + j.parts * rows * dim;
+        float* l = parts.lse + j.parts * rows;
         ++j.parts;
-        e = many ? launch_attn_tc(dtype, p, false, 0, o, l, counter, sm_count, s) : launch_split_any(dtype, p, o, l, true, false, sm_count, s);
+        e = many ? launch_attn_tc(dtype, p, false, 0, o, l, parts.counter, sm_count, s) : launch_split_any(dtype, p, o, l, true, false, sm_count, s);
         return e != cudaSuccess ? e : launch_attn_join(dtype, j, s);
     }
     if (!many) return launch_split_any(dtype, p, nullptr, nullptr, false, false, sm_count, s);
-    int64_t keys = p.kv.table_stride << p.kv.page_shift;
-    if (p.window > 0 && p.window + p.sinks + 256 < keys) keys = p.window + p.sinks + 256;
-    const int64_t pairs = tc_pairs(p.n_tokens, group, p.kv.n_seqs, false) * p.kv.n_heads;
-    const int slots = slots_for(pairs, (keys + 127) / 128, p.kv.n_seqs, rows, spare, sm_count);
-    if (slots == 0) return launch_attn_tc(dtype, p, false, 0, nullptr, nullptr, counter, sm_count, s);
-    if ((e = launch_attn_tc(dtype, p, false, slots, part_o, part_lse, counter, sm_count, s)) != cudaSuccess) return e;
-    j.parts = slots;
+    if (parts.slots == 0) return launch_attn_tc(dtype, p, false, 0, nullptr, nullptr, parts.counter, sm_count, s);
+    if ((e = launch_attn_tc(dtype, p, false, parts.slots, parts.o, parts.lse, parts.counter, sm_count, s)) != cudaSuccess) return e;
+    j.parts = parts.slots;
     return launch_attn_join(dtype, j, s);
 }
 
