@@ -14,9 +14,9 @@ namespace qx {
 constexpr int kUnit = 64;                // keys of a unit
 constexpr uint64_t kSplitWaitNs = 10000000000ull;  // (four_again() over millions of keys may be waited for)
 constexpr int kSplitWarps = 4;
-// A second warpgroup for the producer (its other three warps only give up
-// registers): 128 registers a thread at launch, of which the consumers, who hold
-// a tile's queries and output, take most.
+// A second warpgroup for the producers (in 16 bits one warp, and the other three
+// only give up registers; over codes all four work): 128 registers a thread at
+// launch, of which the consumers, who hold a tile's queries and output, take most.
 constexpr int kSplitThreads = 2 * 32 * kSplitWarps;
 constexpr int kConsumerRegs = 176, kProducerRegs = 80;
 static_assert(kConsumerRegs + kProducerRegs <= 2 * 128, "registers the CTA was launched with");

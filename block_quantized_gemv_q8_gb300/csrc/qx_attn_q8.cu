@@ -14,11 +14,11 @@
 // base counts the scales with the scores.
 //
 // It is bound by DRAM until its instructions take longer.  Measured: 64 tokens over
-// windows of 4096 keys and 4 first ones (8 key heads of 128, bf16, 0.49 GB) 95 us, 5.1
-// TB/s, 75 % of the measured copy rate (without the products 87, without the tiles'
-// ends 83, without either 70); one token over 131072 keys 55.6 us (73 %); one over
-// 1023 keys 8.0; five tokens of 16 sequences over 2000 to 20001 keys, 20 rows, 130 us
-// (46 %).
+// windows of 4096 keys and 4 first ones (8 key heads of 128, bf16, 0.49 GB) 96 us, 5.1
+// TB/s, 74 % of the measured copy rate (without the products 87, without the tiles'
+// ends 83, without either 70); one token over 131072 keys 55.9 us (73 %); one over
+// 1023 keys 8.1; five tokens of 16 sequences over 2000 to 20001 keys, 20 rows, 126 us
+// (47 %).
 #include "qx_attn.cuh"
 #include "qx_attn_codes.cuh"
 #include "qx_attn_line.cuh"

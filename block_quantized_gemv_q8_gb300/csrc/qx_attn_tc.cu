@@ -45,9 +45,9 @@
 // scales for the softmax: a key's multiplies its score, a value's its probability
 // before that is rounded to f16.  The maximum then counts the power of two that the
 // block's scales stay below.  The conversion's shared-memory traffic stands beside the
-// MMAs' and the scalings in a tile's chain: 512 tokens over 16384 keys 188 us (without
-// the conversion 142, without the scalings 158 to 173, without both 116; 16 bits 104),
-// 8191 tokens over the window 191, five chunks of prompts at head size 64 99.
+// MMAs' and the scalings in a tile's chain: 512 tokens over 16384 keys 176 us (at 188,
+// without the conversion 142, without the scalings 158 to 173, without both 116; 16 bits
+// 104), 8191 tokens over the window 194, five chunks of prompts at head size 64 96.
 //
 // Every wait is bounded and reports through the device error word.
 #include <cuda.h>
@@ -1082,7 +1082,7 @@ __global__ void __launch_bounds__(Q8 ? kTcThreadsQ8 : kTcThreads, 1) attn_tc_ker
                     // have been multiplied, so its barrier is in the phase that is asked for.
                     // Before them it may be two uses behind, where this warpgroup had no rows
                     // for a while, and of the same parity.  Asked there, 512 tokens over 16384
-                    // keys took 189 us for 180, and 8191 tokens over the window 195 for 197.)
+                    // keys took 9 us more, and 8191 tokens over the window 2 us less.)
                     if (!(ok = warp_wait(&scale_full[set], set_phase, kv.err, kErrTimeoutMma))) break;
                     if (++set == G::kScaleSets) set = 0, set_phase ^= 1;
                 }

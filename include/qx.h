@@ -487,7 +487,8 @@ size_t qx_attn_scratch_bytes(int64_t n_tokens, int n_q_heads, int n_heads, int h
  * at k_scale[page * scale_page_stride + h * scale_head_stride + slot] (the same
  * for v).  table, kv_len, q_start, positions, padding and what is out of range:
  * as for qx_kv.  A cache may be filled by other means than qx_rope_append_q8:
- * every code, -128 too, and every finite scale are served.
+ * every code, -128 too, and every finite scale are served (the attention's bounds:
+ * for those of values up to 2^100).
  */
 typedef struct {
     int8_t* k;
@@ -518,8 +519,8 @@ qx_status qx_rope_append_q8(const qx_kv_q8* kv, const qx_qkv* in, const float* c
                             int rot, int interleaved, void* q_out, qx_stream_t s);
 
 /* What the cache holds at the positions of the call's tokens: d * code, rounded
- * once to out_dtype (QX_F32, QX_F16 or QX_BF16), to k_out and v_out (device,
- * [n_tokens, n_heads, head_dim]; one of them may be NULL).  With q_start the sums
+ * to f32 and from there to out_dtype (QX_F32, QX_F16 or QX_BF16), to k_out and v_out
+ * (device, [n_tokens, n_heads, head_dim]; one of them may be NULL).  With q_start the sums
  * of kv_len, whole sequences.  Padding tokens get zeros; tokens of no sequence,
  * and those whose page is out of range, are left as they are. */
 qx_status qx_kv_read_q8(const qx_kv_q8* kv, int64_t n_tokens, void* k_out, void* v_out, qx_dtype out_dtype, qx_stream_t s);
@@ -528,16 +529,17 @@ qx_status qx_kv_read_q8(const qx_kv_q8* kv, int64_t n_tokens, void* k_out, void*
  * qx_attn_paged over an 8-bit cache: q and out of kv->dtype (out also QX_F32),
  * the same scratch (qx_attn_scratch_bytes).  Row (t, h)
  *     out = sum_j p_j d^v_j c^v_j / sum_j p_j,   p_j = exp(scale d^k_j q . c^k_j).
- * over the keys that qx_attn_paged lets it see.  Queries and codes are taken as they
- * are; scores, maxima, sums and outputs are held in f32.  q . c^k_j is summed up first;
- * where that sum and the score are in f32's range, the factors between them are of any
- * size (a sum of zero is a score of zero).  At head sizes 64 and 128
- * p_j d^v_j is rounded to f16 (relative 2^-11 at most) before it meets the codes;
- * products below 2^-21 of D, the row's largest p_j times its largest d^v_j (or 2^-80,
+ * over the keys that qx_attn_paged lets it see.  Codes are taken as they are, and so
+ * are queries, but that a bf16 row's elements below 2^-28 of its largest may be held
+ * to 2^-39 of that (head sizes 64 and 128, few rows a sequence); scores, maxima, sums
+ * and outputs are held in f32.  q . c^k_j is summed up first; where that sum and the
+ * score are in f32's range, the factors between them are of any size (a sum of zero
+ * is a score of zero).  At head sizes 64 and 128 p_j d^v_j is rounded to f16
+ * (relative 2^-11 at most) before it meets the codes; products below 2^-21 of D, the row's largest p_j times its largest d^v_j (or 2^-80,
  * where all of them are smaller), are held to 2^-32 of D, and the sum of the p_j holds
  * all of them down to 2^-38 of the largest: for value scales up to 2^100, however far
- * apart.  Smaller ones than 2^-80 alone so lose bits, below 2^-112 all of them.  At
- * other head sizes it stays in f32.
+ * apart.  (Scales that are all below 2^-80 so lose bits, below 2^-112 all of them.)
+ * At other head sizes the products stay in f32.
  * A key that a row does not see does not enter it, whatever its slot holds (NaN and
  * infinities, too), and the bounds above are of the keys that it sees; in which
  * power of two its products are rounded may go by other rows and keys, so a row's
